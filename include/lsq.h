@@ -462,6 +462,97 @@ lsq_status lsq_adamw_step(float* p, const float* g, float* m, float* v, void* p_
 lsq_status lsq_lora_refresh_bf16(const float* p, void* p_bf16, int64_t n, lsq_cuda_stream stream);
 
 /* ------------------------------------------------------------------------
+ * Layers outside the quantised base: LayerNorm, a dense linear with its
+ * epilogue, and 8-bit activation checkpoints.  Trained or unquantised parts
+ * next to the streamed stack (norms, projections, heads).  Activations bf16,
+ * sums and statistics fp32, no atomics (results bit-identical run to run).
+ * Device pointers 16-byte aligned (fp32 vectors of a row index 4-byte); the
+ * feature counts d, N, K multiples of 8; anything else is EINVAL before
+ * anything is enqueued.
+ * ---------------------------------------------------------------------- */
+/* LayerNorm: y = (x - mean) rstd g + b per row, mean and variance over d,
+ * rstd = 1 / sqrt(var + eps) (variance of the centred values, no cancellation).
+ *  x, y     bf16 [rows, d];  g, b bf16 [d] (b may be NULL: no bias)
+ *  mean, rstd  fp32 [rows], kept for the backward (each may be NULL)
+ * d <= 16384, else EUNSUPPORTED. */
+lsq_status lsq_layernorm_fwd(const void* x, const void* g, const void* b, void* y, float* mean, float* rstd,
+                             int64_t rows, int64_t d, float eps, lsq_cuda_stream stream);
+/* Its backward.  With xh = (x - mean) rstd and a = dy g:
+ *   dres_out = dres_in + rstd (a - mean(a) - xh mean(a xh))
+ *   dg (+)= sum over rows of dy xh;   db (+)= sum over rows of dy
+ *  dres_in  bf16 [rows, d], NULL (treated as 0), may alias dres_out
+ *  dg, db   fp32 [d], each may be NULL (frozen)
+ *  accumulate  0: overwrite dg / db, 1: add into them
+ *  workspace   lsq_layernorm_bwd_workspace_size() bytes, 256-byte aligned, for
+ *              the blocks' partial sums; NULL allowed when dg and db are NULL */
+size_t lsq_layernorm_bwd_workspace_size(int64_t rows, int64_t d);
+lsq_status lsq_layernorm_bwd(const void* dy, const void* x, const void* g, const float* mean, const float* rstd,
+                             const void* dres_in, void* dres_out, float* dg, float* db, int32_t accumulate,
+                             int64_t rows, int64_t d, void* workspace, size_t workspace_bytes,
+                             lsq_cuda_stream stream);
+
+/* 8-bit activation checkpoint of a bf16 [rows, d] tensor: per block of 64
+ * columns of a row (the last block of a row may be shorter) the largest
+ * magnitude amax (bf16, exact) and per element an int8 code
+ *   q = sign(x) floor(127 |x| / amax + 1/2),
+ * which stands for bf16_rn(q amax / 127) (code 0 for +0).  A block below 2^-118 is kept as
+ * zeros; a block that holds an infinity or a NaN is restored as NaN (a blown-up
+ * activation stays visible).  Layout: codes [rows][d], then from the next
+ * multiple of 16 bytes amax [rows][ceil(d / 64)]; lsq_ckpt8_size() bytes,
+ * 16-byte aligned, 1.03 bytes per element.  Bit-exact with a CPU
+ * implementation of the definition.  d <= 16384, else EUNSUPPORTED. */
+size_t lsq_ckpt8_size(int64_t rows, int64_t d);
+lsq_status lsq_ckpt8_pack(const void* x, void* ckpt, int64_t rows, int64_t d, lsq_cuda_stream stream);
+lsq_status lsq_ckpt8_unpack(const void* ckpt, void* x, int64_t rows, int64_t d, lsq_cuda_stream stream);
+/* The checkpoint made and used in the RMSNorm passes that read the same rows:
+ *  fwd_pack8:   lsq_rmsnorm_fwd of x that also leaves x's checkpoint (rstd may be NULL)
+ *  fwd_unpack8: restores x (bf16, for the residual) and normalises the restored
+ *               rows: y and rstd are lsq_rmsnorm_fwd's for them (rstd may be NULL)
+ *  bwd_unpack8: lsq_rmsnorm_bwd with the restored rows read from the checkpoint
+ * dres_in may be NULL (treated as 0) or alias dres_out. */
+lsq_status lsq_rmsnorm_fwd_pack8(const void* x, const void* g, void* y, float* rstd, void* ckpt, int64_t rows,
+                                 int64_t d, float eps, lsq_cuda_stream stream);
+lsq_status lsq_rmsnorm_fwd_unpack8(const void* ckpt, const void* g, void* x, void* y, float* rstd, int64_t rows,
+                                   int64_t d, float eps, lsq_cuda_stream stream);
+lsq_status lsq_rmsnorm_bwd_unpack8(const void* dy, const void* ckpt, const void* g, const float* rstd,
+                                   const void* dres_in, void* dres_out, int64_t rows, int64_t d,
+                                   lsq_cuda_stream stream);
+
+/* Dense linear on the tensor cores with everything after the product in its
+ * epilogue (fp32, one rounding):
+ *   z = x W^T + bias,   y = residual + act(z)
+ *  x bf16 [M, K];  w bf16 [N, K];  bias bf16 [N] or NULL
+ *  residual  bf16 [M, N] or NULL; may alias y
+ *  z         bf16 [M, N] or NULL: the pre-activation, kept for the backward
+ *            (must not alias y or residual)
+ *  act       an lsq_act */
+typedef enum lsq_act {
+  LSQ_ACT_NONE = 0,
+  LSQ_ACT_RELU = 1,
+  LSQ_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution function */
+  LSQ_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  LSQ_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} lsq_act;
+lsq_status lsq_linear_fwd(const void* x, const void* w, const void* bias, int32_t act, const void* residual, void* z,
+                          void* y, int64_t M, int64_t N, int64_t K, lsq_cuda_stream stream);
+/* Its backward, given the z that the forward kept (NULL for LSQ_ACT_NONE):
+ *   dz = dy act'(z);  dx = dz W;  dw (+)= dz^T x;  dbias (+)= sum over rows of dz
+ * (the gradient of the residual is dy).  dbias sums the fp32 dz; the two
+ * products take dz rounded to bf16, the tensor cores' operand type.
+ *  dx        bf16 [M, K] or NULL
+ *  dw        [N, K] or NULL: fp32 with dw_f32 = 1, else bf16
+ *  dbias     fp32 [N] or NULL
+ *  accumulate  1: add into dw and dbias (dw then fp32, else EINVAL), 0: overwrite
+ *  workspace   lsq_linear_bwd_workspace_size() bytes, 256-byte aligned (dz and
+ *              the partial sums of dbias); NULL allowed with LSQ_ACT_NONE and
+ *              no dbias
+ * x may be NULL without dw, w without dx. */
+size_t lsq_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act);
+lsq_status lsq_linear_bwd(const void* dy, const void* x, const void* w, const void* z, int32_t act, void* dx, void* dw,
+                          int32_t dw_f32, float* dbias, int32_t accumulate, int64_t M, int64_t N, int64_t K,
+                          void* workspace, size_t workspace_bytes, lsq_cuda_stream stream);
+
+/* ------------------------------------------------------------------------
  * Layer streaming scheduler.
  *
  * The frozen base sits in host RAM and reaches the GPU one decoder layer at a

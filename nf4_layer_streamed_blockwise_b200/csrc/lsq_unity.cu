@@ -6,6 +6,8 @@
 #include "gemm_nf4.cu"
 #include "lora_grad.cu"
 #include "layer_ops.cu"
+#include "norm_ops.cu"
+#include "linear.cu"
 #include "attention_tc.cu"
 #include "attention.cu"
 #include "stream.cu"

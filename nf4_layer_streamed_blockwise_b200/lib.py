@@ -138,6 +138,25 @@ _SIGS = {
     "lsq_lora_refresh_bf16": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p]),
     "lsq_adamw_step": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_float,
                                  c_float, c_float, c_float, c_float, c_void_p]),
+    "lsq_layernorm_fwd": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64,
+                                    c_float, c_void_p]),
+    "lsq_layernorm_bwd_workspace_size": (c_size_t, [c_int64, c_int64]),
+    "lsq_layernorm_bwd": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_int32, c_int64, c_int64, c_void_p, c_size_t, c_void_p]),
+    "lsq_ckpt8_size": (c_size_t, [c_int64, c_int64]),
+    "lsq_ckpt8_pack": (c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_void_p]),
+    "lsq_ckpt8_unpack": (c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_void_p]),
+    "lsq_rmsnorm_fwd_pack8": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_float,
+                                        c_void_p]),
+    "lsq_rmsnorm_fwd_unpack8": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_float,
+                                          c_void_p]),
+    "lsq_rmsnorm_bwd_unpack8": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
+                                          c_int64, c_void_p]),
+    "lsq_linear_fwd": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int64,
+                                 c_int64, c_int64, c_void_p]),
+    "lsq_linear_bwd_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32]),
+    "lsq_linear_bwd": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
+                                 c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_size_t, c_void_p]),
     "lsq_stream_create": (c_int32, [ctypes.POINTER(lsq_stream_cfg), c_void_p, c_void_p, ctypes.POINTER(c_void_p)]),
     "lsq_stream_set_absmax_expand": (c_int32, [c_void_p, ctypes.POINTER(lsq_absmax_dq_item), c_int32, c_size_t]),
     "lsq_layer_upload_async": (c_int32, [c_void_p, c_int32, c_int32]),
@@ -193,7 +212,9 @@ _KERNELS = {"lsq_nf4_quantize": 1, "lsq_nf4_dequantize": 1, "lsq_absmax_double_q
             "lsq_dense_gemm": 1, "lsq_dense_gemm_ex": 1, "lsq_rmsnorm_fwd": 1, "lsq_rmsnorm_bwd": 1, "lsq_rope": 1, "lsq_rope_table": 1,
             "lsq_attention_fwd": 1, "lsq_attention_bwd": 3, "lsq_swiglu_fwd": 1, "lsq_swiglu_bwd": 1,
             "lsq_embed_gather": 1, "lsq_xent_fwd_bwd": 2, "lsq_adamw_step": 1, "lsq_lora_refresh_bf16": 1, "lsq_seq_logprob": 2,
-            "lsq_dpo_loss": 1, "lsq_seq_logprob_bwd": 1, "lsq_wait_flag": 1}
+            "lsq_dpo_loss": 1, "lsq_seq_logprob_bwd": 1, "lsq_wait_flag": 1,
+            "lsq_layernorm_fwd": 1, "lsq_ckpt8_pack": 1, "lsq_ckpt8_unpack": 1, "lsq_rmsnorm_fwd_pack8": 1,
+            "lsq_rmsnorm_fwd_unpack8": 1, "lsq_rmsnorm_bwd_unpack8": 1, "lsq_linear_fwd": 1}
 
 
 def _call(name, *args, launches=None):
@@ -530,6 +551,112 @@ def lsq_adamw_step(p, g, m, v, p_bf16, n: int, step: int, lr: float, beta1: floa
                    weight_decay: float, stream=None):
     _call("lsq_adamw_step", _p(p), _p(g), _p(m), _p(v), _p(p_bf16), n, step, lr, beta1, beta2, eps, weight_decay,
           _stream(stream))
+
+
+# ---------------------------------------------------------------------------- layers outside the quantised base
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
+
+
+def _t(fn: str, name: str, t, dtype, n: int) -> Optional[int]:
+    """Address of a dense tensor of at least n elements of dtype (any dtype when None: n counts bytes) on the
+    current device; None and raw addresses pass through."""
+    if t is None or isinstance(t, int):
+        return t
+    if dtype is None:
+        n = -(-n // t.element_size())
+    elif t.dtype != dtype:
+        raise LsqError(1, fn, f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() < n:
+        raise LsqError(1, fn, f"{name} has {t.numel()} elements, needs {n}")
+    if not t.is_contiguous():
+        raise LsqError(1, fn, f"{name} must be contiguous")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise LsqError(1, fn, f"{name} must be on the current CUDA device, got {t.device}")
+    return t.data_ptr()
+
+
+def lsq_layernorm_fwd(x, g, b, y, mean, rstd, rows: int, d: int, eps: float, stream=None):
+    """y = (x - mean) rstd g + b; b, mean and rstd may be None."""
+    f, n, bf, f32 = "lsq_layernorm_fwd", rows * d, torch.bfloat16, torch.float32
+    _call(f, _t(f, "x", x, bf, n), _t(f, "g", g, bf, d), _t(f, "b", b, bf, d), _t(f, "y", y, bf, n),
+          _t(f, "mean", mean, f32, rows), _t(f, "rstd", rstd, f32, rows), rows, d, eps, _stream(stream))
+
+
+def lsq_layernorm_bwd_workspace_size(rows: int, d: int) -> int:
+    return int(_fn("lsq_layernorm_bwd_workspace_size")(rows, d))
+
+
+def lsq_layernorm_bwd(dy, x, g, mean, rstd, dres_in, dres_out, dg, db, accumulate: int, rows: int, d: int, workspace,
+                      stream=None):
+    """dres_out = dres_in + dx; dg, db fp32 (None: frozen), overwritten or (accumulate=1) added to."""
+    f, n, bf, f32 = "lsq_layernorm_bwd", rows * d, torch.bfloat16, torch.float32
+    grads = dg is not None or db is not None
+    _call(f, _t(f, "dy", dy, bf, n), _t(f, "x", x, bf, n), _t(f, "g", g, bf, d), _t(f, "mean", mean, f32, rows),
+          _t(f, "rstd", rstd, f32, rows), _t(f, "dres_in", dres_in, bf, n), _t(f, "dres_out", dres_out, bf, n),
+          _t(f, "dg", dg, f32, d), _t(f, "db", db, f32, d), accumulate, rows, d,
+          _t(f, "workspace", workspace, None, 0), _nbytes(workspace), _stream(stream), launches=2 if grads else 1)
+
+
+def lsq_ckpt8_size(rows: int, d: int) -> int:
+    """Bytes of the 8-bit checkpoint of a bf16 [rows, d] tensor."""
+    return int(_fn("lsq_ckpt8_size")(rows, d))
+
+
+def lsq_ckpt8_pack(x, ckpt, rows: int, d: int, stream=None):
+    f = "lsq_ckpt8_pack"
+    _call(f, _t(f, "x", x, torch.bfloat16, rows * d), _t(f, "ckpt", ckpt, None, lsq_ckpt8_size(rows, d)), rows, d,
+          _stream(stream))
+
+
+def lsq_ckpt8_unpack(ckpt, x, rows: int, d: int, stream=None):
+    f = "lsq_ckpt8_unpack"
+    _call(f, _t(f, "ckpt", ckpt, None, lsq_ckpt8_size(rows, d)), _t(f, "x", x, torch.bfloat16, rows * d), rows, d,
+          _stream(stream))
+
+
+def lsq_rmsnorm_fwd_pack8(x, g, y, rstd, ckpt, rows: int, d: int, eps: float, stream=None):
+    """lsq_rmsnorm_fwd that also leaves x's 8-bit checkpoint."""
+    f, n, bf = "lsq_rmsnorm_fwd_pack8", rows * d, torch.bfloat16
+    _call(f, _t(f, "x", x, bf, n), _t(f, "g", g, bf, d), _t(f, "y", y, bf, n),
+          _t(f, "rstd", rstd, torch.float32, rows), _t(f, "ckpt", ckpt, None, lsq_ckpt8_size(rows, d)), rows, d, eps,
+          _stream(stream))
+
+
+def lsq_rmsnorm_fwd_unpack8(ckpt, g, x, y, rstd, rows: int, d: int, eps: float, stream=None):
+    """x restored from its 8-bit checkpoint, and lsq_rmsnorm_fwd of it."""
+    f, n, bf = "lsq_rmsnorm_fwd_unpack8", rows * d, torch.bfloat16
+    _call(f, _t(f, "ckpt", ckpt, None, lsq_ckpt8_size(rows, d)), _t(f, "g", g, bf, d), _t(f, "x", x, bf, n),
+          _t(f, "y", y, bf, n), _t(f, "rstd", rstd, torch.float32, rows), rows, d, eps, _stream(stream))
+
+
+def lsq_rmsnorm_bwd_unpack8(dy, ckpt, g, rstd, dres_in, dres_out, rows: int, d: int, stream=None):
+    """lsq_rmsnorm_bwd with x read from its 8-bit checkpoint."""
+    f, n, bf = "lsq_rmsnorm_bwd_unpack8", rows * d, torch.bfloat16
+    _call(f, _t(f, "dy", dy, bf, n), _t(f, "ckpt", ckpt, None, lsq_ckpt8_size(rows, d)), _t(f, "g", g, bf, d),
+          _t(f, "rstd", rstd, torch.float32, rows), _t(f, "dres_in", dres_in, bf, n),
+          _t(f, "dres_out", dres_out, bf, n), rows, d, _stream(stream))
+
+
+def lsq_linear_fwd(x, w, bias, act: int, residual, z, y, M: int, N: int, K: int, stream=None):
+    """y = residual + act(x w^T + bias); z receives the pre-activation; bias, residual and z may be None."""
+    f, mn, bf = "lsq_linear_fwd", M * N, torch.bfloat16
+    _call(f, _t(f, "x", x, bf, M * K), _t(f, "w", w, bf, N * K), _t(f, "bias", bias, bf, N), act,
+          _t(f, "residual", residual, bf, mn), _t(f, "z", z, bf, mn), _t(f, "y", y, bf, mn), M, N, K, _stream(stream))
+
+
+def lsq_linear_bwd_workspace_size(M: int, N: int, K: int, act: int) -> int:
+    return int(_fn("lsq_linear_bwd_workspace_size")(M, N, K, act))
+
+
+def lsq_linear_bwd(dy, x, w, z, act: int, dx, dw, dw_f32: int, dbias, accumulate: int, M: int, N: int, K: int,
+                   workspace, stream=None):
+    """dx, dw and dbias (each may be None) of lsq_linear_fwd from dy and the kept pre-activation z."""
+    f, mn, bf, f32 = "lsq_linear_bwd", M * N, torch.bfloat16, torch.float32
+    launches = (1 if act != ACT_NONE or dbias is not None else 0) + sum(t is not None for t in (dbias, dx, dw))
+    _call(f, _t(f, "dy", dy, bf, mn), _t(f, "x", x, bf, M * K), _t(f, "w", w, bf, N * K), _t(f, "z", z, bf, mn), act,
+          _t(f, "dx", dx, bf, M * K), _t(f, "dw", dw, f32 if dw_f32 else bf, N * K), dw_f32,
+          _t(f, "dbias", dbias, f32, N), accumulate, M, N, K, _t(f, "workspace", workspace, None, 0),
+          _nbytes(workspace), _stream(stream), launches=launches)
 
 
 # ---------------------------------------------------------------------------- streaming

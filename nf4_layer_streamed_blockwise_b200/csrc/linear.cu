@@ -11,6 +11,7 @@
 //   dx       p = k, q = m, c = n:  P = W  MN-major,  Q = dz K-major
 //   dW       p = k, q = n, c = m:  P = x  MN-major,  Q = dz MN-major
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "host_common.h"
@@ -25,46 +26,81 @@ namespace lin {
 using ops::pack8;
 using ops::unpack8;
 
+// One lane of the converged warp, the same each time.  The producer and issuer warps run their loops whole
+// and elect a lane at the asynchronous instructions only: under an `if (lane == 0)` around the loop the compiler
+// cannot keep addresses and descriptors in uniform registers, and a 64-deep block cost 0.26 us of issue
+// whatever the tile's size; so it costs 0.165 (1 x 4096 x 4096 unsplit: 20.8 -> 14.9 us).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+
 // ---------------------------------------------------------------- activations
-// act(z) and act'(z) in fp32 on the fp32 pre-activation.  GELU: z Phi(z), Phi by erfcf on the side where
-// it does not cancel; its tanh form and SiLU are z sigmoid(u), the logistic through expf, which under- and
-// overflows to the right limits.
-__device__ __forceinline__ float logistic(float u) { return 1.0f / (1.0f + expf(-u)); }
-__device__ __forceinline__ float phi_cdf_f(float z) { return 0.5f * erfcf(-0.70710678118654752f * z); }
-constexpr float GT_C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+// act(z) and act'(z) in fp32 on the fp32 pre-activation, through the special-function unit's exp and
+// reciprocal (relative error about 2^-21 here, far below the bf16 rounding that follows; the sums of dbias
+// see it as 2^-21 of their terms).  The logistic under- and overflows to the right limits; infinities, which
+// would meet 0 * inf, are taken out first.  GELU's normal distribution function is Abramowitz & Stegun 7.1.26
+// (|error| <= 1.5e-7 in erf), whose exponential is the density that the derivative needs.
+__device__ __forceinline__ float logistic(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
+// Phi(z); *e = exp(-z^2 / 2)
+__device__ __forceinline__ float normal_cdf(float z, float* e) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  *e = __expf(-0.5f * z * z);
+  const float half = 0.5f * q * t * *e;  // Phi(-|z|)
+  return z < 0.0f ? half : 1.0f - half;
+}
+constexpr float GT_C = 1.5957691216057308f;  // 2 sqrt(2 / pi): z (1 + tanh(u)) / 2 = z logistic(2 u)
 constexpr float GT_A = 0.044715f;
 
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
+  if (ACT == LSQ_ACT_NONE) return z;
   if (ACT == LSQ_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
-  if (ACT == LSQ_ACT_GELU) return z == -INFINITY ? 0.0f : z * phi_cdf_f(z);
-  if (ACT == LSQ_ACT_GELU_TANH) return z == -INFINITY ? 0.0f : z * logistic(GT_C * (z + GT_A * z * z * z));
-  if (ACT == LSQ_ACT_SILU) return z == -INFINITY ? 0.0f : z * logistic(z);
-  return z;
+  float e, f;
+  if (ACT == LSQ_ACT_GELU) f = normal_cdf(z, &e);
+  if (ACT == LSQ_ACT_GELU_TANH) f = logistic(GT_C * (z + GT_A * z * z * z));
+  if (ACT == LSQ_ACT_SILU) f = logistic(z);
+  return z == -INFINITY ? 0.0f : z * f;
 }
 template <int ACT>
 __device__ __forceinline__ float dact_f(float z) {
+  if (ACT == LSQ_ACT_NONE) return 1.0f;
   if (ACT == LSQ_ACT_RELU) return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
-  // beyond |z| = 1e4 every derivative here is 0 or 1 in fp32, and the products below would meet inf * 0
-  if (ACT != LSQ_ACT_NONE && fabsf(z) > 1e4f) return z > 0.0f ? 1.0f : 0.0f;
-  if (ACT == LSQ_ACT_GELU) return phi_cdf_f(z) + z * 0.3989422804014327f * expf(-0.5f * z * z);
+  float e, d;
+  if (ACT == LSQ_ACT_GELU) {
+    d = normal_cdf(z, &e);
+    d = fmaf(z * 0.3989422804014327f, e, d);
+  }
   if (ACT == LSQ_ACT_GELU_TANH) {
     const float s = logistic(GT_C * (z + GT_A * z * z * z));
-    return s + z * s * (1.0f - s) * GT_C * (1.0f + 3.0f * GT_A * z * z);
+    d = fmaf(z * s * (1.0f - s), GT_C * (1.0f + 3.0f * GT_A * z * z), s);
   }
   if (ACT == LSQ_ACT_SILU) {
     const float s = logistic(z);
-    return s * (1.0f + z * (1.0f - s));
+    d = s * fmaf(z, 1.0f - s, 1.0f);
   }
-  return 1.0f;
+  // beyond |z| = 1e4 every derivative here is 0 or 1 in fp32, and the products above meet inf * 0
+  return fabsf(z) > 1e4f ? (z > 0.0f ? 1.0f : 0.0f) : d;
 }
-__device__ __forceinline__ float act_of(int act, float z) {
+template <int ACT, int N>
+__device__ __forceinline__ void act_all(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = act_f<ACT>(v[i]);
+}
+template <int N>
+__device__ __forceinline__ void act_of(int act, float (&v)[N]) {
   switch (act) {
-    case LSQ_ACT_RELU: return act_f<LSQ_ACT_RELU>(z);
-    case LSQ_ACT_GELU: return act_f<LSQ_ACT_GELU>(z);
-    case LSQ_ACT_GELU_TANH: return act_f<LSQ_ACT_GELU_TANH>(z);
-    case LSQ_ACT_SILU: return act_f<LSQ_ACT_SILU>(z);
-    default: return z;
+    case LSQ_ACT_RELU: act_all<LSQ_ACT_RELU>(v); break;
+    case LSQ_ACT_GELU: act_all<LSQ_ACT_GELU>(v); break;
+    case LSQ_ACT_GELU_TANH: act_all<LSQ_ACT_GELU_TANH>(v); break;
+    case LSQ_ACT_SILU: act_all<LSQ_ACT_SILU>(v); break;
+    default: break;
   }
 }
 
@@ -78,7 +114,9 @@ struct Epi {
 
 struct Params {
   int P, Q, nkb;   // output columns and rows, 64-deep contraction blocks
-  int tp, splits;  // 128-column tiles; cluster size (contraction split)
+  int tp, splits;  // 128-column tiles; cluster size (contraction split), a power of two
+  int lper;        // log2 of the rows each CTA of a cluster finishes
+  int bn;          // persistent form: tile columns, a multiple of 32 up to 256
   Epi e;
 };
 struct Maps {
@@ -105,10 +143,7 @@ __device__ __forceinline__ void finish8(float (&v)[8], const Epi& e, int64_t off
     for (int i = 0; i < 8; ++i) v[i] += b[i];
   }
   if (e.z) *reinterpret_cast<uint4*>(e.z + off) = pack8(v);
-  if (e.act != LSQ_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_of(e.act, v[i]);
-  }
+  act_of(e.act, v);
   if (e.residual) {
     float r[8];
     unpack8(*reinterpret_cast<const uint4*>(e.residual + off), r);
@@ -123,8 +158,18 @@ __device__ __forceinline__ void finish8(float (&v)[8], const Epi& e, int64_t off
 // CTAs of a cluster split the contraction, each leaves its fp32 partial tile in the shared memory of the
 // CTA that finishes those rows (BT / S of them), and that CTA adds them in rank order: no atomics, no
 // second kernel, no workspace.
-constexpr int BP = 128, BK = 64, NTHREADS = 192, MAX_S = 8;
+constexpr int BP = 128, BK = 64, NTHREADS = 256, MAX_S = 8;
 constexpr int P_BYTES = BP * BK * 2;
+
+// Descriptor of an operand tile at saddr, and its step per 16 of the contraction (16-byte units).  One thread
+// issues every product: with the descriptors rebuilt for each instruction it took about 590 cycles a block,
+// more than the tensor core needs for 256 columns, so the loops only add constants to these.
+template <int MN>
+__device__ __forceinline__ uint64_t op_desc(uint32_t saddr) {
+  return MN ? smem_desc(saddr, 8192, 1024, 2) : smem_desc(saddr, 16, 1024, 2);
+}
+template <int MN>
+constexpr uint64_t DSTEP = MN ? 2048 / 16 : 32 / 16;
 
 template <int BT>
 struct Cfg {
@@ -172,13 +217,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   // the cluster's CTAs have started once this phase completes (waited for before the exchange)
-  if (S > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   if (warp == 4) {
-    if (lane == 0) {
-      for (int i = kb0; i < kb1; ++i) {
-        const int j = i - kb0, s = j % C::NST;
-        if (!mbar_wait(&empty[s], ((uint32_t)(j / C::NST) & 1u) ^ 1u, 431)) break;
+    int s = 0;
+    uint32_t ph = 1;  // the ring starts empty
+    for (int i = kb0; i < kb1; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph, 431))) break;
+      if (elect_one()) {
         uint8_t* pd = smem + s * C::STAGE;
         uint8_t* qd = pd + P_BYTES;
         mbar_arrive_expect_tx(&full[s], (uint32_t)C::STAGE);
@@ -195,52 +241,53 @@ __global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_
           for (int c = 0; c < BT / 64; ++c) tma_load_2d(qd + c * 8192, &maps.q, &full[s], q0 + c * 64, i * BK);
         }
       }
+      __syncwarp();
+      if (++s == C::NST) s = 0, ph ^= 1;
     }
-    __syncwarp();
   } else if (warp == 5) {
-    if (lane == 0) {
-      const uint32_t id = idesc_bf16(BP, BT, PMN, QMN);
-      for (int i = kb0; i < kb1; ++i) {
-        const int j = i - kb0, s = j % C::NST;
-        if (!mbar_wait(&full[s], (uint32_t)(j / C::NST) & 1u, 531)) break;
-        tc_fence_after();
-        const uint32_t pb = smem_u32(smem + s * C::STAGE), qb = pb + P_BYTES;
+    const uint32_t id = idesc_bf16(BP, BT, PMN, QMN);
+    const uint64_t pd0 = op_desc<PMN>(smem_u32(smem)), qd0 = op_desc<QMN>(smem_u32(smem) + P_BYTES);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = kb0; i < kb1; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, 531))) break;
+      tc_fence_after();
+      const uint64_t at = (uint64_t)(s * (C::STAGE >> 4));
+      if (elect_one()) {
+        tc_mma(tmem, pd0 + at, qd0 + at, id, i != kb0);
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint64_t pd = PMN ? smem_desc(pb + kk * 2048, 8192, 1024, 2) : smem_desc(pb + kk * 32, 16, 1024, 2);
-          const uint64_t qd = QMN ? smem_desc(qb + kk * 2048, 8192, 1024, 2) : smem_desc(qb + kk * 32, 16, 1024, 2);
-          tc_mma(tmem, pd, qd, id, (j | kk) != 0);
-        }
+        for (int kk = 1; kk < BK / 16; ++kk)
+          tc_mma(tmem, pd0 + at + kk * DSTEP<PMN>, qd0 + at + kk * DSTEP<QMN>, id, 1);
         tc_commit(&empty[s]);
       }
-      tc_commit(afull);  // also when a wait gave up: the epilogue is not left waiting
+      __syncwarp();
+      if (++s == C::NST) s = 0, ph ^= 1;
     }
+    if (elect_one()) tc_commit(afull);  // also when a wait gave up: the epilogue is not left waiting
     __syncwarp();
   }
   if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const int per = BT / S;  // output rows this CTA finishes
+  const int lper = p.lper, per = 1 << lper;  // output rows this CTA finishes
   if (warp < 4) {
     const bool ok = __all_sync(0xffffffffu, mbar_wait(afull, 0, 731));
     tc_fence_after();
     if (ok) {
-      const uint32_t lb = (uint32_t)(warp * 32) << 16;
-      const int col = warp * 32 + lane;
-#pragma unroll
+      const uint32_t lb = tmem + ((uint32_t)(warp * 32) << 16);
+      // row r of the tile is finished by rank r >> lper, as its row r & (per - 1).  Rolled: the code runs once
+      // per block, so what counts is the instructions fetched (unrolled eightfold it took 20.5 us, not 9, for
+      // 333 x 1536 x 576)
+      const uint32_t mine = smem_u32(smem + C::OFF_X) + (uint32_t)(((rank << lper) * BP + warp * 32 + lane) * 4);
+#pragma unroll 1
       for (int c = 0; c < BT; c += 16) {
         float v[16];
-        tmem_ld16(tmem + lb + (uint32_t)c, v);
+        tmem_ld16(lb + (uint32_t)c, v);
         tc_wait_ld();
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-          const int r = c + t;  // row of the tile: finished by rank r / per
-          float* dst = reinterpret_cast<float*>(smem + C::OFF_X) + (rank * per + r % per) * BP + col;
-          if (S == 1) {
-            *dst = v[t];
-          } else {
-            uint32_t a;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(dst)), "r"(r / per));
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v[t]) : "memory");
-          }
+          const uint32_t dst = mine + (uint32_t)(((c + t) & (per - 1)) * (BP * 4));
+          uint32_t a;
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(dst), "r"((c + t) >> lper));
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v[t]) : "memory");
         }
       }
     }
@@ -256,6 +303,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_
     tmem_dealloc(tmem, C::TCOLS);
   }
   const float* xs = reinterpret_cast<const float*>(smem + C::OFF_X);
+#pragma unroll 1
   for (int it = threadIdx.x; it < per * (BP / 8); it += NTHREADS) {
     const int r = it / (BP / 8), c = (it % (BP / 8)) * 8;
     const int q = q0 + rank * per + r, col = p0 + c;
@@ -263,14 +311,274 @@ __global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+#pragma unroll 1
     for (int k = 0; k < S; ++k) {  // rank order
-      const float4* a = reinterpret_cast<const float4*>(xs + (k * per + r) * BP + c);
+      const float4* a = reinterpret_cast<const float4*>(xs + ((k << lper) + r) * BP + c);
       const float4 lo = a[0], hi = a[1];
       v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
       v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
     }
     finish8(v, p.e, (int64_t)q * p.P + col, col);
   }
+}
+
+// ---------------------------------------------------------------- persistent form
+// For outputs of many tiles.  A cluster of two CTAs on two SMs computes 256 rows x bn columns (cta_group::2:
+// each CTA stages its 128 rows and half of the columns, 32 KB per 64-deep block where a lone CTA's 128 x 256
+// tile takes 48: the single-CTA form ran at the rate L2 fed it, 1370 TFLOP/s for 2048 x 14336 x 4096).
+// Clusters walk tiles c, c + C, ... (row tile fastest, so those that share a slice of P run together); two
+// TMEM accumulators alternate, so the epilogue of a tile runs under the products of the next.  Warps 0-7:
+// epilogue (warp w: the 32 rows of TMEM lanes 32 (w % 4), every other 32-column piece from piece w / 4 on:
+// two warps per scheduler, since the activations cost about as much as the products of a short
+// contraction); warp 8: TMA producer; warp 9: MMA issuer (leader).  Each 32 x 32 piece is staged in shared
+// memory (swizzled, no bank conflicts) and leaves by TMA, which clips the edges; an accumulated fp32
+// output leaves as a TMA reduction (one addend per element and call: the order of adds is that of the calls).
+constexpr int TM = 256, GST = 6, GTHREADS = 320, EPI_WARPS = 8;
+constexpr int GA_BYTES = 128 * BK * 2, GSTAGE = 2 * GA_BYTES;
+constexpr int G_OFF_STG = GST * GSTAGE;
+constexpr int STG_BYTES = 2048;  // one bf16 piece; an fp32 piece takes both of a warp's buffers
+constexpr int G_OFF_BAR = G_OFF_STG + EPI_WARPS * 2 * STG_BYTES;
+constexpr int G_OFF_MISC = G_OFF_BAR + 8 * (2 * GST + 5);
+constexpr int G_BYTES = G_OFF_MISC + 16 + 1024;
+static_assert(G_BYTES <= 232448, "shared memory");
+
+struct GMaps {
+  CUtensorMap a, b, out, z;  // a: Q side (rows of the output), b: P side (columns)
+};
+
+// TMA add of a staged box into fp32 global memory, in the thread's current bulk group
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* m, const void* src, int x, int y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+}
+
+template <int AMN, int BMN, int F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GTHREADS, 1)
+    linear_pair_kernel(const __grid_constant__ GMaps maps, const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G_OFF_BAR);  // the leader's: both CTAs' loads
+  uint64_t* empty = full + GST;
+  uint64_t* tfull = empty + GST;
+  uint64_t* tempty = tfull + 2;  // the leader's: both CTAs' epilogue warps
+  uint64_t* drain = tempty + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + G_OFF_MISC);
+  const uint32_t rank = nf4g::cluster_ctarank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ntm = (p.Q + TM - 1) / TM, tiles = ntm * ((p.P + p.bn - 1) / p.bn);
+  const int cid = (int)(blockIdx.x >> 1), ncl = (int)(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < GST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    nf4g::tmem_alloc_pair(s_tmem, 512);
+    nf4g::tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  nf4g::cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp == 8) {
+    const int hb = p.bn / 2, nbox = (hb + 63) / 64;  // this CTA's columns; 64-wide boxes of an MN-major P
+    const uint32_t bytes = 2u * (uint32_t)(GA_BYTES + (BMN ? nbox * 8192 : hb * 128));
+    const uint32_t full0 = nf4g::cluster_addr(full, 0);
+    int s = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int t = cid; ok && t < tiles; t += ncl) {
+      const int m0 = (t % ntm) * TM + (int)rank * 128, n0 = (t / ntm) * p.bn + (int)rank * hb;
+      for (int i = 0; i < p.nkb; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ph, 441));
+        if (!ok) break;
+        if (elect_one()) {
+          uint8_t* ad = smem + s * GSTAGE;
+          uint8_t* bd = ad + GA_BYTES;
+          const uint32_t fl = full0 + (uint32_t)s * 8;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          if (!AMN) {
+            nf4g::tma_load_2d_pair(ad, &maps.a, fl, i * BK, m0);
+          } else {
+            nf4g::tma_load_2d_pair(ad, &maps.a, fl, m0, i * BK);
+            nf4g::tma_load_2d_pair(ad + 8192, &maps.a, fl, m0 + 64, i * BK);
+          }
+          if (!BMN) {
+            nf4g::tma_load_2d_pair(bd, &maps.b, fl, i * BK, n0);
+          } else {
+            nf4g::tma_load_2d_pair(bd, &maps.b, fl, n0, i * BK);
+            if (nbox > 1) nf4g::tma_load_2d_pair(bd + 8192, &maps.b, fl, n0 + 64, i * BK);
+          }
+        }
+        __syncwarp();
+        if (++s == GST) s = 0, ph ^= 1;
+      }
+    }
+  } else if (warp == 9) {
+    if (rank == 0) {
+      const uint32_t id = idesc_bf16(TM, p.bn, AMN, BMN);
+      const uint64_t ad0 = op_desc<AMN>(smem_u32(smem)), bd0 = op_desc<BMN>(smem_u32(smem) + GA_BYTES);
+      int s = 0, j = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = cid; ok && t < tiles; t += ncl, ++j) {
+        const int buf = j & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, 541));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * 256);
+        for (int i = 0; i < p.nkb; ++i) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ph, 542));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t at = (uint64_t)(s * (GSTAGE >> 4));
+          if (elect_one()) {
+            nf4g::tc_mma_pair(d, ad0 + at, bd0 + at, id, i != 0);
+#pragma unroll
+            for (int kk = 1; kk < BK / 16; ++kk)
+              nf4g::tc_mma_pair(d, ad0 + at + kk * DSTEP<AMN>, bd0 + at + kk * DSTEP<BMN>, id, 1);
+            nf4g::tc_commit_pair_mc(&empty[s], 0x3);
+          }
+          __syncwarp();
+          if (++s == GST) s = 0, ph ^= 1;
+        }
+        if (ok && elect_one()) nf4g::tc_commit_pair_mc(&tfull[buf], 0x3);
+        __syncwarp();
+      }
+      if (!ok) {
+        if (elect_one()) nf4g::tc_commit_pair(drain);
+        __syncwarp();
+        mbar_wait(drain, 0, 543);
+      }
+    }
+  } else {
+    const Epi& e = p.e;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int wg = warp >> 2;
+    uint8_t* stg = smem + G_OFF_STG + warp * 2 * STG_BYTES;
+    int j = 0, k = 0;
+    for (int t = cid; t < tiles; t += ncl, ++j) {
+      const int row0 = (t % ntm) * TM + (int)rank * 128 + (warp & 3) * 32, n0 = (t / ntm) * p.bn;
+      const int buf = j & 1, row = row0 + lane;
+      const int nc = row0 < p.Q ? (min(p.bn, p.P - n0) + 31) / 32 : 0;  // 32-column pieces inside the output
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u, 741))) break;
+      tc_fence_after();
+      for (int c = wg; c < nc; c += 2) {
+        const int col = n0 + c * 32;
+        uint4 rv[4];
+        if (!F32 && e.residual) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            rv[q] = (row < p.Q && col + q * 8 < p.P)
+                        ? *reinterpret_cast<const uint4*>(e.residual + (int64_t)row * p.P + col + q * 8)
+                        : make_uint4(0u, 0u, 0u, 0u);
+        }
+        float v[32];
+        tmem_ld32(tmem + lane_base + (uint32_t)(buf * 256 + c * 32), v);
+        tc_wait_ld_regs(v);
+        if (c + 2 >= nc) {  // this warp's part of the accumulator is in registers: hand it back
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) nf4g::mbar_arrive_cluster(nf4g::cluster_addr(&tempty[buf], 0));
+        }
+        if (F32) {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          dense::stage_row<1>(v, smem_u32(stg) + (uint32_t)lane * 128, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (e.accumulate) tma_add_2d(&maps.out, stg, col, row0);
+            else tma_store_2d(&maps.out, stg, col, row0);
+            bulk_commit();
+          }
+          continue;
+        }
+        if (e.bias) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (col + q * 8 >= p.P) break;
+            float b[8];
+            unpack8(*reinterpret_cast<const uint4*>(e.bias + col + q * 8), b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[q * 8 + i] += b[i];
+          }
+        }
+        if (e.z) {
+          if (lane == 0) bulk_wait_read<1>();  // the piece before last has left this buffer
+          __syncwarp();
+          dense::stage_row<0>(v, smem_u32(stg + k * STG_BYTES) + (uint32_t)lane * 64, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&maps.z, stg + k * STG_BYTES, col, row0);
+            bulk_commit();
+          }
+          k ^= 1;
+        }
+        act_of(e.act, v);
+        if (e.residual) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float r[8];
+            unpack8(rv[q], r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[q * 8 + i] += r[i];
+          }
+        }
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+        dense::stage_row<0>(v, smem_u32(stg + k * STG_BYTES) + (uint32_t)lane * 64, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&maps.out, stg + k * STG_BYTES, col, row0);
+          bulk_commit();
+        }
+        k ^= 1;
+      }
+      if (wg >= nc) {  // no piece of this tile is this warp's
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) nf4g::mbar_arrive_cluster(nf4g::cluster_addr(&tempty[buf], 0));
+      }
+    }
+    if (lane == 0) bulk_wait_all();  // the staged stores are written before the CTA exits
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  nf4g::cluster_sync_all();
+  if (warp == 9) {
+    tc_fence_after();
+    nf4g::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int AMN, int BMN, int F32>
+static lsq_status launch_pair(const GMaps& maps, const Params& p, int64_t tiles, cudaStream_t stream) {
+  static int configured[64] = {0};
+  int dev = 0;
+  LSQ_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev >= 0 && dev < 64 && !configured[dev]) {
+    LSQ_CUDA_TRY(
+        cudaFuncSetAttribute(linear_pair_kernel<AMN, BMN, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, G_BYTES));
+    configured[dev] = 1;
+  }
+  const unsigned ncl = (unsigned)std::min<int64_t>(tiles, num_sms() / 2);
+  linear_pair_kernel<AMN, BMN, F32><<<2 * ncl, GTHREADS, G_BYTES, stream>>>(maps, p);
+  LSQ_LAUNCH_CHECK("linear_pair_kernel");
+  return LSQ_OK;
 }
 
 // K-major operand [rows, C] with box {64, brows}; MN-major operand [C, rows] with box {64, 64}
@@ -307,23 +615,83 @@ static lsq_status launch_split(const Maps& maps, const Params& p, int64_t cluste
   return LSQ_OK;
 }
 
+// Which form a product takes, and its tile: the smallest estimate in us, from measurements of both forms on
+// B200 (graph replays, 19 shapes from 1 x 4568 x 104 to 8192 x 5120 x 2048, every tile of each form):
+//  * one tile per cluster, per round of the CTAs that fit: 0.16 + 0.0006 bt a 64-deep block (what L2 feeds one
+//    SM) and 3.9 + 0.02 bt of start, exchange and stores.  1 x 4096 x 4096: 15.8 unsplit, 10.1 in two, 7.2 in
+//    four (persistent: 19.2); 130 x 4096 x 4096: 14.2 with 128 rows in two (17.6).
+//  * persistent: 4.5, and per round of the pairs the longer of products and epilogue plus a fifth of the
+//    shorter.  A block costs 0.345 at 256 columns (the tensor cores, at the clock that the power cap leaves
+//    them), in proportion to the columns down to 0.235 (what L2 feeds them); an MN-major P whose half tile is
+//    no multiple of the 64-wide boxes loads columns that it does not use, 0.05 more.  Narrower tiles pay where
+//    they fill the last round: 2048 x 14336 x 4096 takes 159.6 with 224 columns (6.9 rounds of 74 pairs), 166.2
+//    with 256 (6.05); 512 x 4096 x 4096 18.6 with 128, 24.8 with 256 (one cluster a tile: 22.2).
+struct Plan {
+  int pair, bt, splits, bn;
+};
+static Plan plan_product(int64_t P, int64_t Q, int nkb, int pmn, int qmn) {
+  const double sms = num_sms();
+  Plan best{};
+  double tb = 1e30;
+  const int64_t tp = (P + BP - 1) / BP;
+  for (int bt = qmn ? 64 : 16; bt <= 128; bt *= 2) {
+    const double tiles = (double)(tp * ((Q + bt - 1) / bt));
+    for (int S = 1; S <= MAX_S && S <= nkb; S *= 2) {
+      const double fit = S <= 2 ? sms : S == 4 ? sms - sms / 9 : sms - sms / 7;  // clusters do not straddle GPCs
+      const double t = std::ceil(tiles * S / fit) * ((0.16 + 0.0006 * bt) * ((nkb + S - 1) / S) + 3.9 + 0.02 * bt);
+      if (t < tb) tb = t, best = Plan{0, bt, S, 0};
+    }
+  }
+  for (int bn = 256; bn >= 128; bn -= 32) {
+    const double rounds = std::ceil((double)(((Q + TM - 1) / TM) * ((P + bn - 1) / bn)) / (sms / 2));
+    const double prod = nkb * (std::max(0.235, 0.345 * bn / 256) + (pmn && bn / 2 % 64 ? 0.05 : 0.0));
+    const double epi = 0.3 + 1.55 * bn / 256;
+    const double t = 4.5 + rounds * (std::max(prod, epi) + 0.2 * std::min(prod, epi));
+    if (t < tb) tb = t, best = Plan{1, 0, 0, bn};
+  }
+  return best;
+}
+
 // out[Q, P] = sum over C of the operands (see the top), with the epilogue e
 template <int PMN, int QMN>
 static lsq_status product(const void* pop, const void* qop, int64_t P, int64_t Q, int64_t C, const Epi& e,
                           cudaStream_t stream) {
-  const int bt = QMN ? (Q <= 64 ? 64 : 128) : Q <= 16 ? 16 : Q <= 32 ? 32 : Q <= 64 ? 64 : 128;
   Params p{};
   p.P = (int)P;
   p.Q = (int)Q;
   p.nkb = (int)((C + BK - 1) / BK);  // the tail reads as zeros (TMA out-of-bounds fill)
   p.tp = (int)((P + BP - 1) / BP);
   p.e = e;
+  const Plan plan = plan_product(P, Q, p.nkb, PMN, QMN);
+  lsq_status st;
+  if (plan.pair) {
+    p.bn = plan.bn;
+    GMaps gm;
+    memset(&gm, 0, sizeof(gm));
+    st = map_operand(&gm.a, qop, QMN, Q, C, TM / 2);
+    if (st == LSQ_OK) st = map_operand(&gm.b, pop, PMN, P, C, p.bn / 2);
+    if (st == LSQ_OK)
+      st = e.f32 ? encode_tmap_2d(&gm.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, e.out, P, Q, P * 4, 32, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_128B)
+                 : encode_tmap_2d(&gm.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, e.out, P, Q, P * 2, 32, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_64B);
+    if (st == LSQ_OK && e.z)
+      st = encode_tmap_2d(&gm.z, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, e.z, P, Q, P * 2, 32, 32,
+                          CU_TENSOR_MAP_SWIZZLE_64B);
+    if (st != LSQ_OK) return st;
+    const int64_t tiles = ((Q + TM - 1) / TM) * ((P + p.bn - 1) / p.bn);
+    if constexpr (QMN)
+      if (e.f32) return launch_pair<QMN, PMN, 1>(gm, p, tiles, stream);
+    return launch_pair<QMN, PMN, 0>(gm, p, tiles, stream);
+  }
+  const int bt = plan.bt;
+  p.splits = plan.splits;
+  p.lper = (bt == 16 ? 4 : bt == 32 ? 5 : bt == 64 ? 6 : 7) -
+           (p.splits == 1 ? 0 : p.splits == 2 ? 1 : p.splits == 4 ? 2 : 3);
   const int64_t tiles = (int64_t)p.tp * ((Q + bt - 1) / bt);
-  p.splits = 1;
-  while (p.splits < MAX_S && tiles * p.splits * 2 <= num_sms() && p.nkb >= p.splits * 4) p.splits *= 2;
   Maps maps;
   memset(&maps, 0, sizeof(maps));
-  lsq_status st = map_operand(&maps.p, pop, PMN, P, C, BP);
+  st = map_operand(&maps.p, pop, PMN, P, C, BP);
   if (st == LSQ_OK) st = map_operand(&maps.q, qop, QMN, Q, C, bt);
   if (st != LSQ_OK) return st;
   if constexpr (!QMN) {

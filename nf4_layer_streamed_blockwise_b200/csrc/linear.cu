@@ -37,61 +37,97 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // ---------------------------------------------------------------- activations
-// act(z) and act'(z) in fp32 on the fp32 pre-activation, through the special-function unit's exp and
-// reciprocal (relative error about 2^-21 here, far below the bf16 rounding that follows; the sums of dbias
-// see it as 2^-21 of their terms).  The logistic under- and overflows to the right limits; infinities, which
-// would meet 0 * inf, are taken out first.  GELU's normal distribution function is Abramowitz & Stegun 7.1.26
+// act(z) and act'(z) in fp32 on the fp32 pre-activation, two values at a time (f32x2; scalar, the derivative
+// of GELU took longer than its bytes: 67 us, not 53, for 8192 x 5120), through the special-function unit's
+// exp2 and reciprocal (relative error about 2^-22, far below the bf16 rounding that follows; the sums of
+// dbias see it as 2^-22 of their terms).  The logistic under- and overflows to the right limits; what would
+// meet 0 * inf is taken out at the end.  GELU's normal distribution function is Abramowitz & Stegun 7.1.26
 // (|error| <= 1.5e-7 in erf), whose exponential is the density that the derivative needs.
-__device__ __forceinline__ float logistic(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
-// Phi(z); *e = exp(-z^2 / 2)
-__device__ __forceinline__ float normal_cdf(float z, float* e) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  *e = __expf(-0.5f * z * z);
-  const float half = 0.5f * q * t * *e;  // Phi(-|z|)
-  return z < 0.0f ? half : 1.0f - half;
+__device__ __forceinline__ float ex2_f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+__device__ __forceinline__ float rcp_f(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t both(float x) { return f2(x, x); }
+__device__ __forceinline__ uint64_t ex2_2(uint64_t x) {
+  const float2 f = f2split(x);
+  return f2(ex2_f(f.x), ex2_f(f.y));
+}
+__device__ __forceinline__ uint64_t rcp_2(uint64_t x) {
+  const float2 f = f2split(x);
+  return f2(rcp_f(f.x), rcp_f(f.y));
+}
+constexpr float LOG2E = 1.4426950408889634f;
 constexpr float GT_C = 1.5957691216057308f;  // 2 sqrt(2 / pi): z (1 + tanh(u)) / 2 = z logistic(2 u)
 constexpr float GT_A = 0.044715f;
-
-template <int ACT>
-__device__ __forceinline__ float act_f(float z) {
-  if (ACT == LSQ_ACT_NONE) return z;
-  if (ACT == LSQ_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
-  float e, f;
-  if (ACT == LSQ_ACT_GELU) f = normal_cdf(z, &e);
-  if (ACT == LSQ_ACT_GELU_TANH) f = logistic(GT_C * (z + GT_A * z * z * z));
-  if (ACT == LSQ_ACT_SILU) f = logistic(z);
-  return z == -INFINITY ? 0.0f : z * f;
+// logistic(u) with v = -u log2(e)
+__device__ __forceinline__ uint64_t logistic2(uint64_t v) { return rcp_2(add2(ex2_2(v), both(1.0f))); }
+__device__ __forceinline__ uint64_t gelu_tanh_arg(uint64_t z) {
+  return mul2(z, fma2(mul2(z, z), both(-LOG2E * GT_C * GT_A), both(-LOG2E * GT_C)));
+}
+// Phi(z); e = exp(-z^2 / 2)
+__device__ __forceinline__ uint64_t normal_cdf2(uint64_t z, uint64_t& e) {
+  const uint64_t az = z & 0x7fffffff7fffffffull;
+  const uint64_t t = rcp_2(fma2(az, both(0.3275911f * 0.70710678118654752f), both(1.0f)));
+  uint64_t q = fma2(both(1.061405429f * 0.5f), t, both(-1.453152027f * 0.5f));
+  q = fma2(q, t, both(1.421413741f * 0.5f));
+  q = fma2(q, t, both(-0.284496736f * 0.5f));
+  q = fma2(q, t, both(0.254829592f * 0.5f));
+  e = ex2_2(mul2(mul2(z, z), both(-0.5f * LOG2E)));
+  // Phi = 1/2 +- (1/2 - Phi(-|z|)), the sign z's
+  const uint64_t h = fma2(mul2(q, t), e ^ 0x8000000080000000ull, both(0.5f));
+  return add2(both(0.5f), h ^ (z & 0x8000000080000000ull));
 }
 template <int ACT>
-__device__ __forceinline__ float dact_f(float z) {
-  if (ACT == LSQ_ACT_NONE) return 1.0f;
-  if (ACT == LSQ_ACT_RELU) return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
-  float e, d;
+__device__ __forceinline__ uint64_t act2(uint64_t z) {
+  if (ACT == LSQ_ACT_NONE) return z;
+  const float2 f = f2split(z);
+  if (ACT == LSQ_ACT_RELU) return f2(f.x < 0.0f ? 0.0f : f.x, f.y < 0.0f ? 0.0f : f.y);  // a NaN stays one
+  uint64_t e, s;
+  if (ACT == LSQ_ACT_GELU) s = normal_cdf2(z, e);
+  if (ACT == LSQ_ACT_GELU_TANH) s = logistic2(gelu_tanh_arg(z));
+  if (ACT == LSQ_ACT_SILU) s = logistic2(mul2(z, both(-LOG2E)));
+  const float2 y = f2split(mul2(z, s));
+  return f2(f.x == -INFINITY ? 0.0f : y.x, f.y == -INFINITY ? 0.0f : y.y);
+}
+template <int ACT>
+__device__ __forceinline__ uint64_t dact2(uint64_t z) {
+  if (ACT == LSQ_ACT_NONE) return both(1.0f);
+  const float2 f = f2split(z);
+  if (ACT == LSQ_ACT_RELU)
+    return f2(f.x > 0.0f ? 1.0f : (f.x == f.x ? 0.0f : f.x), f.y > 0.0f ? 1.0f : (f.y == f.y ? 0.0f : f.y));
+  uint64_t e, d;
   if (ACT == LSQ_ACT_GELU) {
-    d = normal_cdf(z, &e);
-    d = fmaf(z * 0.3989422804014327f, e, d);
+    d = normal_cdf2(z, e);
+    d = fma2(mul2(z, both(0.3989422804014327f)), e, d);
   }
-  if (ACT == LSQ_ACT_GELU_TANH) {
-    const float s = logistic(GT_C * (z + GT_A * z * z * z));
-    d = fmaf(z * s * (1.0f - s), GT_C * (1.0f + 3.0f * GT_A * z * z), s);
+  if (ACT == LSQ_ACT_GELU_TANH) {  // s + z s (1 - s) u'
+    const uint64_t s = logistic2(gelu_tanh_arg(z));
+    const uint64_t du = fma2(mul2(z, z), both(3.0f * GT_C * GT_A), both(GT_C));
+    d = fma2(mul2(mul2(z, s), du), add2(both(1.0f), s ^ 0x8000000080000000ull), s);
   }
-  if (ACT == LSQ_ACT_SILU) {
-    const float s = logistic(z);
-    d = s * fmaf(z, 1.0f - s, 1.0f);
+  if (ACT == LSQ_ACT_SILU) {  // s (1 + z (1 - s))
+    const uint64_t s = logistic2(mul2(z, both(-LOG2E)));
+    d = mul2(s, fma2(z, add2(both(1.0f), s ^ 0x8000000080000000ull), both(1.0f)));
   }
   // beyond |z| = 1e4 every derivative here is 0 or 1 in fp32, and the products above meet inf * 0
-  return fabsf(z) > 1e4f ? (z > 0.0f ? 1.0f : 0.0f) : d;
+  const float2 y = f2split(d);
+  return f2(fabsf(f.x) > 1e4f ? (f.x > 0.0f ? 1.0f : 0.0f) : y.x, fabsf(f.y) > 1e4f ? (f.y > 0.0f ? 1.0f : 0.0f) : y.y);
 }
+
 template <int ACT, int N>
 __device__ __forceinline__ void act_all(float (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = act_f<ACT>(v[i]);
+  for (int i = 0; i < N; i += 2) {
+    const float2 y = f2split(act2<ACT>(f2(v[i], v[i + 1])));
+    v[i] = y.x;
+    v[i + 1] = y.y;
+  }
 }
 template <int N>
 __device__ __forceinline__ void act_of(int act, float (&v)[N]) {
@@ -707,32 +743,33 @@ static lsq_status product(const void* pop, const void* qop, int64_t P, int64_t Q
 // a warp covers 256 columns of a row (16 bytes a lane), a block's eight warps take rows in turn, and the
 // strips' sums are added in order by col_sum_kernel.
 template <int ACT>
-__global__ void __launch_bounds__(256) dz_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ z,
+__global__ void __launch_bounds__(256, 4) dz_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ z,
                                                  uint4* __restrict__ dz, float* __restrict__ part, int64_t rows, int n8,
                                                  int64_t strip) {
   __shared__ float comb[8][32][9];
+  nrm::grid_release();
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + l;
   const int64_t r0 = blockIdx.y * strip, r1 = r0 + strip < rows ? r0 + strip : rows;
-  float s[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = 0.0f;
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
   if (c < n8) {
-#pragma unroll 2
+#pragma unroll 4
     for (int64_t r = r0 + w; r < r1; r += 8) {
-      float d[8];
-      unpack8(dy[r * n8 + c], d);
+      uint64_t d[4];
+      nrm::unpack_pairs(dy[r * n8 + c], d);
       if (ACT != LSQ_ACT_NONE) {
-        float zv[8];
-        unpack8(z[r * n8 + c], zv);
+        uint64_t zv[4];
+        nrm::unpack_pairs(z[r * n8 + c], zv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] *= dact_f<ACT>(zv[j]);
-        dz[r * n8 + c] = pack8(d);
+        for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], dact2<ACT>(zv[j]));
+        dz[r * n8 + c] = nrm::pack_pairs(d);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] += d[j];
+      for (int j = 0; j < 4; ++j) acc[j] = add2(acc[j], d[j]);
     }
   }
+  float s[8];
+  nrm::split8(acc, s);
   if (!part) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) comb[w][l][j] = s[j];
@@ -747,10 +784,10 @@ __global__ void __launch_bounds__(256) dz_kernel(const uint4* __restrict__ dy, c
   o[1] = make_float4(s[4], s[5], s[6], s[7]);
 }
 
-// row strips of dz_kernel: about eight blocks per SM, at least 8 rows each
+// row strips of dz_kernel: one round of its blocks (four per SM), at least 8 rows each
 static int64_t strips_of(int64_t M, int64_t N) {
   const int64_t cb = (N + 255) / 256;
-  const int64_t want = std::max<int64_t>(1, (8 * num_sms() + cb - 1) / cb);
+  const int64_t want = std::max<int64_t>(1, 4 * num_sms() / cb);
   const int64_t rows = std::max<int64_t>(8, (M + want - 1) / want);
   return (M + rows - 1) / rows;
 }

@@ -21,6 +21,11 @@ constexpr int64_t MAX_D = 16384;  // 2048 words: 512 threads x 4, or 1024 x 2
 enum { NONE = 0, RMS = 1, LAYER = 2 };
 enum { BF16 = 0, CKPT8 = 1 };
 
+// Programmatic launch: a kernel that called grid_release lets a dependent launch start early; the dependent's
+// grid_wait returns once that kernel has finished and its writes are visible.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -36,17 +41,6 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   if (l == 0) red[w] = v;
   __syncthreads();
   return warp_sum(l < (int)(blockDim.x >> 5) ? red[l] : 0.0f);
-}
-template <bool WARP>
-__device__ __forceinline__ float2 row_sum2(float a, float b, float2* red) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (WARP) return make_float2(a, b);
-  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  if (l == 0) red[w] = make_float2(a, b);
-  __syncthreads();
-  const float2 t = l < (int)(blockDim.x >> 5) ? red[l] : make_float2(0.0f, 0.0f);
-  return make_float2(warp_sum(t.x), warp_sum(t.y));
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoint
@@ -279,141 +273,307 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) rms_bwd_unpa
   }
 }
 
-// LayerNorm: out = res + rs (a - mean(a) - xh mean(a xh)), a = dy g, xh = (x - mean) rs.  Blocks walk
-// the rows in strides and a thread's columns stay the same, so the sums over rows of dy xh and dy
-// (dg, db) collect in registers and leave once per block; col_sum_kernel adds the blocks in order.
-template <int V, bool WARP, bool GRADS>
-__global__ void __launch_bounds__(WARP ? 256 : 512) ln_bwd_kernel(const __grid_constant__ Bwd p) {
-  __shared__ float2 red[2][32];
-  __shared__ float comb[WARP ? 8 * 32 * 9 : 1];
-  const int T = WARP ? 32 : (int)blockDim.x;
-  const int t = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
-  const int nw = (int)(blockDim.x >> 5), w = (int)(threadIdx.x >> 5);
-  const int64_t first = WARP ? (int64_t)blockIdx.x * nw + w : (int64_t)blockIdx.x;
-  const int64_t step = WARP ? (int64_t)gridDim.x * nw : (int64_t)gridDim.x;
+// LayerNorm: out = res + rs (a - mean(a) - xh mean(a xh)), a = dy g, xh = (x - mean) rs.  Warps (d <= 768)
+// or blocks walk the rows in strides and a thread's columns stay the same, so the sums over rows of dy xh
+// and dy (dg, db) collect in registers and leave once per block; col_sum_kernel adds the blocks in order.
+// The arithmetic runs on pairs (f32x2): scalar, its 30 operations an element took as long as the loads.
+__device__ __forceinline__ void unpack_pairs(uint4 v, uint64_t (&f)[4]) {
+  f[0] = f2(bf16lo(v.x), bf16hi(v.x));
+  f[1] = f2(bf16lo(v.y), bf16hi(v.y));
+  f[2] = f2(bf16lo(v.z), bf16hi(v.z));
+  f[3] = f2(bf16lo(v.w), bf16hi(v.w));
+}
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&f)[4]) {
+  return make_uint4(pack_bf16x2(f[0]), pack_bf16x2(f[1]), pack_bf16x2(f[2]), pack_bf16x2(f[3]));
+}
+// one word of the first pass: xh and a, their row sums, and the column sums of dy xh and dy
+template <bool GRADS>
+__device__ __forceinline__ void ln_bwd_word(uint4 x, uint4 dy, uint4 g, uint64_t nmu, uint64_t rs, uint64_t (&xh)[4],
+                                            uint64_t (&a)[4], uint64_t& s1, uint64_t& s2, uint64_t* sg, uint64_t* sb) {
+  uint64_t d[4];
+  unpack_pairs(x, xh);
+  unpack_pairs(dy, d);
+  unpack_pairs(g, a);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    xh[j] = mul2(add2(xh[j], nmu), rs);
+    a[j] = mul2(d[j], a[j]);
+    s1 = add2(s1, a[j]);
+    s2 = fma2(a[j], xh[j], s2);
+    if (GRADS) {
+      sg[j] = fma2(d[j], xh[j], sg[j]);
+      sb[j] = add2(sb[j], d[j]);
+    }
+  }
+}
+// and of the second: res + rs a - rs m1 - xh rs m2
+__device__ __forceinline__ uint4 ln_bwd_out(const uint64_t (&xh)[4], const uint64_t (&a)[4], uint4 res, uint64_t rs,
+                                            uint64_t nk1, uint64_t nk2) {
+  uint64_t o[4];
+  unpack_pairs(res, o);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = fma2(xh[j], nk2, add2(fma2(a[j], rs, o[j]), nk1));
+  return pack_pairs(o);
+}
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+  const float2 f = f2split(v);
+  return f.x + f.y;
+}
+// this thread's eight column sums of word c, to the block's partial row or (one block) to dg / db
+__device__ __forceinline__ void ln_put_sums(const Bwd& p, int h, int c, const float (&v)[8]) {
+  const bool one = gridDim.x == 1;
+  const int d = p.d8 * 8;
+  float* o = one ? (h ? p.db : p.dg) : p.part + ((int64_t)blockIdx.x * 2 + h) * d;
+  if (!o) return;
+  float4* o4 = reinterpret_cast<float4*>(o + c * 8);
+  float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
+  if (one && p.accumulate) {
+    const float4 x = o4[0], y = o4[1];
+    lo.x += x.x; lo.y += x.y; lo.z += x.z; lo.w += x.w;
+    hi.x += y.x; hi.y += y.y; hi.z += y.z; hi.w += y.w;
+  }
+  o4[0] = lo;
+  o4[1] = hi;
+}
+__device__ __forceinline__ void split8(const uint64_t* s, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = f2split(s[j]);
+    v[2 * j] = f.x;
+    v[2 * j + 1] = f.y;
+  }
+}
+
+// The rows of x, dy and the residual gradient come through rings of shared-memory stages filled by bulk
+// copies, one ring per row walker (a warp or a block), so that the bytes in flight do not depend on the
+// registers, which the sums take: with the loads in registers 8192 x 5120 took 103 us and 16384 x 576 34.
+__device__ __forceinline__ void ln_fetch(const Bwd& p, uint8_t* b, uint64_t* bar, uint32_t rb, int64_t row) {
+  mbar_arrive_expect_tx(bar, rb * (p.res ? 3u : 2u));
+  bulk_g2s(b, p.x + row * p.d8, rb, bar);
+  bulk_g2s(b + rb, p.dy + row * p.d8, rb, bar);
+  if (p.res) bulk_g2s(b + 2 * rb, p.res + row * p.d8, rb, bar);
+}
+
+// a row per warp, V words a lane
+constexpr int LNW = 8;
+template <int V, bool GRADS>
+__global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_constant__ Bwd p, int nst, int stage) {
+  extern __shared__ __align__(128) uint8_t smem[];  // per warp [nst][x | dy | res], then every stage's barrier
+  if (GRADS) grid_release();
+  __shared__ float comb[LNW * 32 * 9];
+  const int t = (int)(threadIdx.x & 31), w = (int)(threadIdx.x >> 5);
+  uint8_t* ring = smem + (size_t)w * nst * stage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)LNW * nst * stage) + w * nst;
   const int d8 = p.d8;
+  const uint32_t rb = (uint32_t)d8 * 16;
   const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-  // V = 4 (block rows): the sums take 64 registers, so gain and residual are loaded at their use
-  constexpr bool LATE = !WARP && V == 4;
-  uint4 gk[LATE ? 1 : V];
-  if (!LATE) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) gk[LATE ? 0 : i] = t + i * T < d8 ? p.g[t + i * T] : z;
+  const int64_t first = (int64_t)blockIdx.x * LNW + w, step = (int64_t)gridDim.x * LNW;
+  if (t == 0) {
+    for (int s = 0; s < nst; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+    for (int s = 0; s < nst; ++s)
+      if (first + s * step < p.rows) ln_fetch(p, ring + (size_t)s * stage, &full[s], rb, first + s * step);
   }
-  auto gain = [&](int i) { return LATE ? (t + i * T < d8 ? p.g[t + i * T] : z) : gk[LATE ? 0 : i]; };
-  float sg[GRADS ? V : 1][8], sb[GRADS ? V : 1][8];
-  if (GRADS) {
+  __syncwarp();
+  uint4 gv[V];
+  uint64_t sg[GRADS ? V : 1][4], sb[GRADS ? V : 1][4];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i) {
+    gv[i] = t + i * 32 < d8 ? p.g[t + i * 32] : z;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sg[i][j] = sb[i][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) sg[GRADS ? i : 0][j] = sb[GRADS ? i : 0][j] = 0ull;
   }
-  int flip = 0;
+  int s = 0;
+  uint32_t ph = 0;
+  bool ok = true;  // after a wait that gave up, the rest of the rows is not waited for
+  for (int64_t row = first; row < p.rows; row += step) {
+    const float mu = p.mean[row], r = p.rstd[row];
+    if (ok) ok = mbar_wait(&full[s], ph, 461);
+    const uint4* b = reinterpret_cast<const uint4*>(ring + (size_t)s * stage);
+    const uint64_t nmu = f2(-mu, -mu), rs = f2(r, r);
+    uint64_t xh[4], a[4], s1 = 0ull, s2 = 0ull;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {  // padded words: dy = g = 0
+      const int c = t + i * 32;
+      const bool in = c < d8;
+      ln_bwd_word<GRADS>(in ? b[c] : z, in ? b[d8 + c] : z, gv[i], nmu, rs, xh, a, s1, s2, sg[GRADS ? i : 0],
+                         sb[GRADS ? i : 0]);
+    }
+    const float k1 = -r * warp_sum(pair_sum(s1)) * p.inv_d, k2 = -r * warp_sum(pair_sum(s2)) * p.inv_d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {  // xh and a again: kept for every word they would not fit the registers
+      const int c = t + i * 32;
+      if (c >= d8) break;
+      uint64_t u1 = 0ull, u2 = 0ull;
+      ln_bwd_word<false>(b[c], b[d8 + c], gv[i], nmu, rs, xh, a, u1, u2, nullptr, nullptr);
+      p.out[row * d8 + c] = ln_bwd_out(xh, a, p.res ? b[2 * d8 + c] : z, rs, f2(k1, k1), f2(k2, k2));
+    }
+    __syncwarp();  // the warp is done with the stage: refill it
+    if (t == 0 && row + nst * step < p.rows)
+      ln_fetch(p, ring + (size_t)s * stage, &full[s], rb, row + nst * step);
+    if (++s == nst) s = 0, ph ^= 1;
+  }
+  if (!GRADS) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // the warps' sums, in warp order; row stride 9 keeps the banks apart
+      float v[8];
+      split8(h ? sb[GRADS ? i : 0] : sg[GRADS ? i : 0], v);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) comb[(w * 32 + t) * 9 + j] = v[j];
+      __syncthreads();
+      const int c = t + i * 32;
+      if (w != 0 || c >= d8) continue;
+      for (int k = 1; k < LNW; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += comb[(k * 32 + t) * 9 + j];
+      ln_put_sums(p, h, c, v);
+    }
+  }
+}
+
+// a row per block, V words a thread.  A stage is refilled once the barrier of the following row has passed:
+// every thread is then done with it.
+template <int V, bool GRADS>
+__global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
+    ln_bwd_block_kernel(const __grid_constant__ Bwd p, int nst, int stage) {
+  extern __shared__ __align__(128) uint8_t ring[];  // [nst][x | dy | res], then the stages' barriers
+  if (GRADS) grid_release();
+  __shared__ float2 red[2][16];
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)nst * stage);
+  const int T = (int)blockDim.x, t = (int)threadIdx.x, d8 = p.d8, nw = T >> 5, lane = t & 31;
+  const uint32_t rb = (uint32_t)d8 * 16;
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  const int64_t first = blockIdx.x, step = gridDim.x;
+  if (t == 0) {
+    for (int s = 0; s < nst; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+    for (int s = 0; s < nst; ++s)
+      if (first + s * step < p.rows) ln_fetch(p, ring + (size_t)s * stage, &full[s], rb, first + s * step);
+  }
+  __syncthreads();
+  uint64_t sg[GRADS ? V : 1][4], sb[GRADS ? V : 1][4];
+  uint4 gv[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    gv[i] = t + i * T < d8 ? p.g[t + i * T] : z;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sg[GRADS ? i : 0][j] = sb[GRADS ? i : 0][j] = 0ull;
+  }
+  int s = 0, flip = 0;
+  uint32_t ph = 0;
+  bool ok = true;  // after a wait that gave up, the rest of the rows is not waited for
   for (int64_t row = first; row < p.rows; row += step, flip ^= 1) {
-    const int64_t base = row * d8;
-    uint4 xv[V], dv[V], rv[LATE ? 1 : V];
+    const float mu = p.mean[row], r = p.rstd[row];
+    if (ok) ok = mbar_wait(&full[s], ph, 461);
+    const uint4* b = reinterpret_cast<const uint4*>(ring + (size_t)s * stage);
+    const uint64_t nmu = f2(-mu, -mu), rs = f2(r, r);
+    uint64_t xh[4], a[4], s1 = 0ull, s2 = 0ull;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = t + i * T;
       const bool in = c < d8;
-      xv[i] = in ? p.x[base + c] : z;
-      dv[i] = in ? p.dy[base + c] : z;
-      if (!LATE) rv[LATE ? 0 : i] = (in && p.res) ? p.res[base + c] : z;
+      ln_bwd_word<GRADS>(in ? b[c] : z, in ? b[d8 + c] : z, gv[i], nmu, rs, xh, a, s1, s2, sg[GRADS ? i : 0],
+                         sb[GRADS ? i : 0]);
     }
-    const float mu = p.mean[row], rs = p.rstd[row];
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float f[8], d[8], g[8];
-      unpack8(xv[i], f);
-      unpack8(dv[i], d);
-      unpack8(gain(i), g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {  // padded columns: d = g = 0
-        const float xh = (f[j] - mu) * rs, a = d[j] * g[j];
-        s1 += a;
-        s2 = fmaf(a, xh, s2);
-        if (GRADS) {
-          sg[i][j] = fmaf(d[j], xh, sg[i][j]);
-          sb[i][j] += d[j];
-        }
-      }
+    // the row's two sums: warps by shuffles, then every thread adds the warps' (two buffers, one barrier a row)
+    const float w1 = warp_sum(pair_sum(s1)), w2 = warp_sum(pair_sum(s2));
+    if (lane == 0) red[flip][t >> 5] = make_float2(w1, w2);
+    __syncthreads();
+    if (t == 0 && row != first) {  // the previous row's stage
+      const int64_t next = row + (nst - 1) * step;
+      const int prev = s == 0 ? nst - 1 : s - 1;
+      if (next < p.rows) ln_fetch(p, ring + (size_t)prev * stage, &full[prev], rb, next);
     }
-    const float2 s = row_sum2<WARP>(s1, s2, red[flip]);
-    const float m1 = s.x * p.inv_d, m2 = s.y * p.inv_d;
+    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < nw; ++i) {
+      const float2 v = red[flip][i];
+      sum.x += v.x;
+      sum.y += v.y;
+    }
+    const float k1 = -r * sum.x * p.inv_d, k2 = -r * sum.y * p.inv_d;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V; ++i) {  // xh and a again: kept for every word they would not fit the registers
       const int c = t + i * T;
       if (c >= d8) break;
-      float f[8], d[8], g[8], o[8];
-      unpack8(xv[i], f);
-      unpack8(dv[i], d);
-      unpack8(gain(i), g);
-      unpack8(LATE ? (p.res ? p.res[base + c] : z) : rv[LATE ? 0 : i], o);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] += rs * (d[j] * g[j] - m1 - (f[j] - mu) * rs * m2);
-      p.out[base + c] = pack8(o);
+      uint64_t u1 = 0ull, u2 = 0ull;
+      ln_bwd_word<false>(b[c], b[d8 + c], gv[i], nmu, rs, xh, a, u1, u2, nullptr, nullptr);
+      p.out[row * d8 + c] = ln_bwd_out(xh, a, p.res ? b[2 * d8 + c] : z, rs, f2(k1, k1), f2(k2, k2));
     }
+    if (++s == nst) s = 0, ph ^= 1;
   }
   if (!GRADS) return;
-  const int d = d8 * 8;
-  const bool one = gridDim.x == 1;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = h ? sb[i][j] : sg[i][j];
-      if (WARP) {  // the warps' sums, in warp order; row stride 9 keeps the banks apart
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) comb[(w * 32 + t) * 9 + j] = v[j];
-        __syncthreads();
-        if (w != 0) continue;
-        for (int k = 1; k < nw; ++k)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += comb[(k * 32 + t) * 9 + j];
-      }
-      const int c = t + i * T;
-      if (c >= d8) continue;
-      float* o = one ? (h ? p.db : p.dg) : p.part + ((int64_t)blockIdx.x * 2 + h) * d;
-      if (!o) continue;
-      float4* o4 = reinterpret_cast<float4*>(o + c * 8);
-      if (one && p.accumulate) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += o[c * 8 + j];
-      }
-      o4[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o4[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
+    const int c = t + i * T;
+    if (c >= d8) break;
+    float v[8];
+    split8(sg[GRADS ? i : 0], v);
+    ln_put_sums(p, 0, c, v);
+    split8(sb[GRADS ? i : 0], v);
+    ln_put_sums(p, 1, c, v);
   }
 }
 
 // out0[c] (+)= sum over the G rows of part[.][c] for c < n0, out1[c - n0] for the columns from n0 on
-// (either may be null); part has row stride ld.  16 warps take rows w, w + 16, ..., added in warp order.
-__global__ void __launch_bounds__(512) col_sum_kernel(const float* __restrict__ part, int G, int64_t ld, int64_t n0,
-                                                      int64_t ncols, float* out0, float* out1, int accumulate) {
-  __shared__ float s[16][33];
+// (either may be null; n0 and ncols even); part has row stride ld.  Warp w of 32 takes rows w, w + 32, ...,
+// eight loads in flight, and the warps' sums are added in order.
+__global__ void __launch_bounds__(1024) col_sum_kernel(const float* __restrict__ part, int G, int64_t ld, int64_t n0,
+                                                       int64_t ncols, float* out0, float* out1, int accumulate) {
+  __shared__ float2 s[32][33];
+  grid_wait();  // launched while the kernel that writes part still runs
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  const int64_t c = (int64_t)blockIdx.x * 32 + l;
-  float v = 0.0f;
+  const int64_t c = ((int64_t)blockIdx.x * 32 + l) * 2;
+  float2 v = make_float2(0.0f, 0.0f);
   if (c < ncols)
-    for (int r = w; r < G; r += 16) v += part[r * ld + c];
+    for (int r0 = w; r0 < G; r0 += 256) {
+      float2 u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        u[i] = r0 + i * 32 < G ? *reinterpret_cast<const float2*>(part + (r0 + i * 32) * ld + c)
+                               : make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v.x += u[i].x;
+        v.y += u[i].y;
+      }
+    }
   s[w][l] = v;
   __syncthreads();
   if (w != 0 || c >= ncols) return;
-  float tot = 0.0f;
+  float2 tot = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) tot += s[k][l];
+  for (int k = 0; k < 32; ++k) {
+    tot.x += s[k][l].x;
+    tot.y += s[k][l].y;
+  }
   float* o = c < n0 ? (out0 ? out0 + c : nullptr) : (out1 ? out1 + (c - n0) : nullptr);
-  if (o) *o = accumulate ? *o + tot : tot;
+  if (!o) return;
+  if (accumulate) {
+    tot.x += o[0];
+    tot.y += o[1];
+  }
+  o[0] = tot.x;
+  o[1] = tot.y;
 }
 
 lsq_status col_sum(const float* part, int G, int64_t ld, int64_t n0, int64_t ncols, float* out0, float* out1,
                    int accumulate, cudaStream_t stream) {
-  col_sum_kernel<<<(unsigned)((ncols + 31) / 32), 512, 0, stream>>>(part, G, ld, n0, ncols, out0, out1, accumulate);
-  LSQ_LAUNCH_CHECK("col_sum_kernel");
+  // programmatic launch: its blocks are set up behind the running kernel's, 4 -> 2 us for a short sum
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)((ncols + 63) / 64));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  LSQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, col_sum_kernel, part, G, ld, n0, ncols, out0, out1, accumulate));
   return LSQ_OK;
 }
 
@@ -439,20 +599,29 @@ static Geo fwd_geo(int64_t rows, int d8) {
   g.blocks = (unsigned)rows;
   return g;
 }
-static Geo ln_bwd_geo(int64_t rows, int d8) {
-  Geo g;
-  g.warp = d8 <= 128;
-  int per = 1, occ;
+// Backward: a row a warp (eight warps a block) or a row a block; `occ` blocks per SM hide one another's row
+// reductions (two blocks of 320 threads: 63 us for 8192 x 5120; one block of two such groups, which halves
+// the partial sums: 72) and share its registers and shared memory (rings of nst stages of `stage` bytes).
+struct BwdGeo {
+  int v, threads, warp, nst, stage;
+  unsigned blocks;
+};
+constexpr int RING_BYTES = 200 * 1024;
+static BwdGeo ln_bwd_geo(int64_t rows, int d8) {
+  BwdGeo g{};
+  g.stage = (3 * d8 * 16 + 127) / 128 * 128;
+  g.warp = d8 <= 96;
+  const int per = g.warp ? LNW : 1;
+  int occ = 2;
   if (g.warp) {
-    g.v = d8 <= 32 ? 1 : d8 <= 64 ? 2 : 4;
-    g.threads = 256;
-    per = 8;
-    occ = 2;
+    g.v = (d8 + 31) / 32;
+    g.threads = LNW * 32;
   } else {
-    g.v = d8 <= 512 ? 1 : d8 <= 1024 ? 2 : 4;
+    g.v = d8 <= 640 ? 2 : 4;
     g.threads = (((d8 + g.v - 1) / g.v) + 31) / 32 * 32;
-    occ = g.threads <= 256 ? 4 : 2;
+    occ = g.v == 4 ? (g.threads <= 256 ? 2 : 1) : std::max(2, std::min(6, 640 / g.threads));
   }
+  g.nst = std::max(2, std::min(8, RING_BYTES / occ / per / g.stage));
   g.blocks = (unsigned)std::min<int64_t>((rows + per - 1) / per, (int64_t)occ * num_sms());
   return g;
 }
@@ -475,6 +644,36 @@ static lsq_status run_fwd(Fwd p, int64_t rows, int64_t d, const char* what, cuda
   }
   LSQ_LAUNCH_CHECK(what);
   return LSQ_OK;
+}
+
+template <typename K>
+static lsq_status ring_smem(K kernel, int* configured) {
+  int dev = 0;
+  LSQ_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64 || configured[dev]) return LSQ_OK;
+  LSQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES + 1024));
+  configured[dev] = 1;
+  return LSQ_OK;
+}
+template <int V, bool WARP, bool GRADS>
+static lsq_status run_ln_bwd(const Bwd& p, const BwdGeo& g, cudaStream_t s) {
+  static int configured[64] = {0};
+  const size_t smem = (size_t)g.nst * (g.stage + 8) * (WARP ? LNW : 1);
+  if constexpr (WARP) {
+    lsq_status st = ring_smem(ln_bwd_warp_kernel<V, GRADS>, configured);
+    if (st != LSQ_OK) return st;
+    ln_bwd_warp_kernel<V, GRADS><<<g.blocks, g.threads, smem, s>>>(p, g.nst, g.stage);
+  } else {
+    lsq_status st = ring_smem(ln_bwd_block_kernel<V, GRADS>, configured);
+    if (st != LSQ_OK) return st;
+    ln_bwd_block_kernel<V, GRADS><<<g.blocks, g.threads, smem, s>>>(p, g.nst, g.stage);
+  }
+  LSQ_LAUNCH_CHECK("ln_bwd kernel");
+  return LSQ_OK;
+}
+template <int V, bool WARP>
+static lsq_status run_ln_bwd(const Bwd& p, bool grads, const BwdGeo& g, cudaStream_t s) {
+  return grads ? run_ln_bwd<V, WARP, true>(p, g, s) : run_ln_bwd<V, WARP, false>(p, g, s);
 }
 
 // the shape and alignment rules of the section, with this file's limits
@@ -516,7 +715,7 @@ extern "C" lsq_status lsq_layernorm_fwd(const void* x, const void* g, const void
 
 extern "C" size_t lsq_layernorm_bwd_workspace_size(int64_t rows, int64_t d) {
   if (rows < 1 || d < 8 || d > nrm::MAX_D) return 256;
-  const nrm::Geo g = nrm::ln_bwd_geo(rows, (int)(d / 8));
+  const nrm::BwdGeo g = nrm::ln_bwd_geo(rows, (int)(d / 8));
   return ((size_t)g.blocks * 2 * (size_t)d * sizeof(float) + 255) / 256 * 256;
 }
 
@@ -548,22 +747,15 @@ extern "C" lsq_status lsq_layernorm_bwd(const void* dy, const void* x, const voi
   p.d8 = (int)(d / 8);
   p.accumulate = accumulate ? 1 : 0;
   p.inv_d = 1.0f / (float)d;
-  const nrm::Geo ge = nrm::ln_bwd_geo(rows, p.d8);
+  const nrm::BwdGeo ge = nrm::ln_bwd_geo(rows, p.d8);
   cudaStream_t s = (cudaStream_t)stream;
-#define LSQ_LN_BWD(V, W)                                                                     \
-  (grads ? nrm::ln_bwd_kernel<V, W, true><<<ge.blocks, ge.threads, 0, s>>>(p)                \
-         : nrm::ln_bwd_kernel<V, W, false><<<ge.blocks, ge.threads, 0, s>>>(p))
-  if (ge.warp) {
-    if (ge.v == 1) LSQ_LN_BWD(1, true);
-    else if (ge.v == 2) LSQ_LN_BWD(2, true);
-    else LSQ_LN_BWD(4, true);
-  } else {
-    if (ge.v == 1) LSQ_LN_BWD(1, false);
-    else if (ge.v == 2) LSQ_LN_BWD(2, false);
-    else LSQ_LN_BWD(4, false);
-  }
-#undef LSQ_LN_BWD
-  LSQ_LAUNCH_CHECK("ln_bwd_kernel");
+  if (ge.warp)
+    st = ge.v == 1   ? nrm::run_ln_bwd<1, true>(p, grads, ge, s)
+         : ge.v == 2 ? nrm::run_ln_bwd<2, true>(p, grads, ge, s)
+                     : nrm::run_ln_bwd<3, true>(p, grads, ge, s);
+  else
+    st = ge.v == 2 ? nrm::run_ln_bwd<2, false>(p, grads, ge, s) : nrm::run_ln_bwd<4, false>(p, grads, ge, s);
+  if (st != LSQ_OK) return st;
   if (!grads || ge.blocks == 1) return LSQ_OK;
   return nrm::col_sum(p.part, (int)ge.blocks, 2 * d, d, 2 * d, dg, db, p.accumulate, s);
 }

@@ -615,8 +615,8 @@ def lsq_layernorm_bwd(dy, x, g, mean, rstd, dres_in, dres_out, dg, db, accumulat
                       stream=None):
     """dres_out = dres_in + dx; dg, db fp32 (None: frozen), overwritten or (accumulate=1) added to."""
     f, dev, n, bf, f32 = "lsq_layernorm_bwd", _dev(), rows * d, torch.bfloat16, torch.float32
-    # one block's sums need no second kernel: one row, or up to eight of at most 1024 columns
-    two = (dg is not None or db is not None) and rows > (8 if d <= 1024 else 1)
+    # the rows of one block (16 of at most 1024 columns; fewer of longer rows) need no second kernel
+    two = (dg is not None or db is not None) and lsq_layernorm_bwd_workspace_size(rows, d) > -(-8 * d // 256) * 256
     _call(f, _t(f, "dy", dy, bf, n, dev), _t(f, "x", x, bf, n, dev), _t(f, "g", g, bf, d, dev),
           _t(f, "mean", mean, f32, rows, dev), _t(f, "rstd", rstd, f32, rows, dev),
           _t(f, "dres_in", dres_in, bf, n, dev), _t(f, "dres_out", dres_out, bf, n, dev), _t(f, "dg", dg, f32, d, dev),

@@ -32,7 +32,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 // sum over the threads of a row, fixed tree, in every thread; a block row needs red[32] and one barrier
-// (the caller alternates between two buffers, so no second one)
 template <bool WARP>
 __device__ __forceinline__ float row_sum(float v, float* red) {
   v = warp_sum(v);
@@ -41,6 +40,21 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   if (l == 0) red[w] = v;
   __syncthreads();
   return warp_sum(l < (int)(blockDim.x >> 5) ? red[l] : 0.0f);
+}
+
+// eight values as four f32x2 pairs
+__device__ __forceinline__ void unpack_pairs(uint4 v, uint64_t (&f)[4]) {
+  f[0] = f2(bf16lo(v.x), bf16hi(v.x));
+  f[1] = f2(bf16lo(v.y), bf16hi(v.y));
+  f[2] = f2(bf16lo(v.z), bf16hi(v.z));
+  f[3] = f2(bf16lo(v.w), bf16hi(v.w));
+}
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&f)[4]) {
+  return make_uint4(pack_bf16x2(f[0]), pack_bf16x2(f[1]), pack_bf16x2(f[2]), pack_bf16x2(f[3]));
+}
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+  const float2 f = f2split(v);
+  return f.x + f.y;
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoint
@@ -163,48 +177,66 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) row_fwd_kern
       }
     }
   }
-  if (NORM == NONE) return;
-  float mu = 0.0f, ss = 0.0f;
-  if (NORM == LAYER) {  // the mean first, then the centred squares: no cancellation
-    float s = 0.0f;
+  if constexpr (NORM == LAYER) {  // the mean first, then the centred squares: no cancellation
+    uint64_t f[V][4], acc = 0ull;  // the row in fp32 pairs: scalar, 8192 x 5120 took 34.2 us, not 32.2
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      unpack_pairs(xv[i], f[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc = add2(acc, f[i][j]);
+    }
+    const float mu = row_sum<WARP>(pair_sum(acc), red[0]) * p.inv_d;
+    const uint64_t nmu = f2(-mu, -mu);
+    acc = 0ull;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (t + i * T >= d8) break;  // the padding is not centred
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[i][j] = add2(f[i][j], nmu);
+        acc = fma2(f[i][j], f[i][j], acc);
+      }
+    }
+    const float rs = 1.0f / sqrtf(row_sum<WARP>(pair_sum(acc), red[1]) * p.inv_d + p.eps);
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mu;
+      if (p.rstd) p.rstd[row] = rs;
+    }
+    const uint64_t rs2 = f2(rs, rs);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * T;
+      if (c >= d8) break;
+      uint64_t g[4], b[4];
+      unpack_pairs(p.g[c], g);
+      unpack_pairs(p.b ? p.b[c] : make_uint4(0u, 0u, 0u, 0u), b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[i][j] = fma2(mul2(f[i][j], rs2), g[j], b[j]);
+      p.y[base + c] = pack_pairs(f[i]);
+    }
+  }
+  if constexpr (NORM == RMS) {
+    float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float f[8];
       unpack8(xv[i], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += f[j];
+      for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
     }
-    mu = row_sum<WARP>(s, red[0]) * p.inv_d;
-  }
+    const float rs = 1.0f / sqrtf(row_sum<WARP>(ss, red[0]) * p.inv_d + p.eps);
+    if (t == 0 && p.rstd) p.rstd[row] = rs;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (NORM == LAYER && t + i * T >= d8) break;  // the padding is not centred
-    float f[8];
-    unpack8(xv[i], f);
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * T;
+      if (c >= d8) break;
+      float f[8], gv[8];
+      unpack8(xv[i], f);
+      unpack8(p.g[c], gv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(f[j] - mu, f[j] - mu, ss);
-  }
-  const float rs = 1.0f / sqrtf(row_sum<WARP>(ss, red[1]) * p.inv_d + p.eps);
-  if (t == 0) {
-    if (p.mean) p.mean[row] = mu;
-    if (p.rstd) p.rstd[row] = rs;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = t + i * T;
-    if (c >= d8) break;
-    float f[8], gv[8], bv[8];
-    unpack8(xv[i], f);
-    unpack8(p.g[c], gv);
-    if (NORM == LAYER && p.b) {
-      unpack8(p.b[c], bv);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - mu) * rs, gv[j], bv[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = (f[j] - mu) * rs * gv[j];
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * rs * gv[j];
+      p.y[base + c] = pack8(f);
     }
-    p.y[base + c] = pack8(f);
   }
 }
 
@@ -247,29 +279,30 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) rms_bwd_unpa
     rv[i] = (in && p.res) ? p.res[base + c] : z;
   }
   const float rs = p.rstd[row];
-  float dot = 0.0f;
+  uint64_t f[V][4], a[V][4], acc = 0ull;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    float f[8], d[8], g[8];
-    unpack8(decode8(cv[i], av[i]), f);
-    unpack8(dv[i], d);
-    unpack8(gv[i], g);
+    uint64_t g[4];
+    unpack_pairs(decode8(cv[i], av[i]), f[i]);
+    unpack_pairs(dv[i], a[i]);
+    unpack_pairs(gv[i], g);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dot = fmaf(d[j] * g[j], f[j], dot);
+    for (int j = 0; j < 4; ++j) {
+      a[i][j] = mul2(a[i][j], g[j]);
+      acc = fma2(a[i][j], f[i][j], acc);
+    }
   }
-  const float k = rs * rs * rs * row_sum<WARP>(dot, red) * p.inv_d;
+  const float k = -rs * rs * rs * row_sum<WARP>(pair_sum(acc), red) * p.inv_d;
+  const uint64_t rs2 = f2(rs, rs), k2 = f2(k, k);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + i * T;
     if (c >= d8) break;
-    float f[8], d[8], g[8], o[8];
-    unpack8(decode8(cv[i], av[i]), f);
-    unpack8(dv[i], d);
-    unpack8(gv[i], g);
-    unpack8(rv[i], o);
+    uint64_t o[4];
+    unpack_pairs(rv[i], o);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] += rs * d[j] * g[j] - f[j] * k;
-    p.out[base + c] = pack8(o);
+    for (int j = 0; j < 4; ++j) o[j] = fma2(f[i][j], k2, fma2(a[i][j], rs2, o[j]));
+    p.out[base + c] = pack_pairs(o);
   }
 }
 
@@ -277,15 +310,6 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) rms_bwd_unpa
 // or blocks walk the rows in strides and a thread's columns stay the same, so the sums over rows of dy xh
 // and dy (dg, db) collect in registers and leave once per block; col_sum_kernel adds the blocks in order.
 // The arithmetic runs on pairs (f32x2): scalar, its 30 operations an element took as long as the loads.
-__device__ __forceinline__ void unpack_pairs(uint4 v, uint64_t (&f)[4]) {
-  f[0] = f2(bf16lo(v.x), bf16hi(v.x));
-  f[1] = f2(bf16lo(v.y), bf16hi(v.y));
-  f[2] = f2(bf16lo(v.z), bf16hi(v.z));
-  f[3] = f2(bf16lo(v.w), bf16hi(v.w));
-}
-__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&f)[4]) {
-  return make_uint4(pack_bf16x2(f[0]), pack_bf16x2(f[1]), pack_bf16x2(f[2]), pack_bf16x2(f[3]));
-}
 // one word of the first pass: xh and a, their row sums, and the column sums of dy xh and dy
 template <bool GRADS>
 __device__ __forceinline__ void ln_bwd_word(uint4 x, uint4 dy, uint4 g, uint64_t nmu, uint64_t rs, uint64_t (&xh)[4],
@@ -314,10 +338,6 @@ __device__ __forceinline__ uint4 ln_bwd_out(const uint64_t (&xh)[4], const uint6
 #pragma unroll
   for (int j = 0; j < 4; ++j) o[j] = fma2(xh[j], nk2, add2(fma2(a[j], rs, o[j]), nk1));
   return pack_pairs(o);
-}
-__device__ __forceinline__ float pair_sum(uint64_t v) {
-  const float2 f = f2split(v);
-  return f.x + f.y;
 }
 // this thread's eight column sums of word c, to the block's partial row or (one block) to dg / db
 __device__ __forceinline__ void ln_put_sums(const Bwd& p, int h, int c, const float (&v)[8]) {
@@ -413,23 +433,24 @@ __global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_c
       ln_fetch(p, ring + (size_t)s * stage, &full[s], rb, row + nst * step);
     if (++s == nst) s = 0, ph ^= 1;
   }
-  if (!GRADS) return;
+  if constexpr (GRADS) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V; ++i) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // the warps' sums, in warp order; row stride 9 keeps the banks apart
-      float v[8];
-      split8(h ? sb[GRADS ? i : 0] : sg[GRADS ? i : 0], v);
-      __syncthreads();
+      for (int h = 0; h < 2; ++h) {  // the warps' sums, in warp order; row stride 9 keeps the banks apart
+        float v[8];
+        split8(h ? sb[GRADS ? i : 0] : sg[GRADS ? i : 0], v);
+        __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) comb[(w * 32 + t) * 9 + j] = v[j];
-      __syncthreads();
-      const int c = t + i * 32;
-      if (w != 0 || c >= d8) continue;
-      for (int k = 1; k < LNW; ++k)
+        for (int j = 0; j < 8; ++j) comb[(w * 32 + t) * 9 + j] = v[j];
+        __syncthreads();
+        const int c = t + i * 32;
+        if (w != 0 || c >= d8) continue;
+        for (int k = 1; k < LNW; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += comb[(k * 32 + t) * 9 + j];
-      ln_put_sums(p, h, c, v);
+          for (int j = 0; j < 8; ++j) v[j] += comb[(k * 32 + t) * 9 + j];
+        ln_put_sums(p, h, c, v);
+      }
     }
   }
 }
@@ -505,16 +526,17 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
     }
     if (++s == nst) s = 0, ph ^= 1;
   }
-  if (!GRADS) return;
+  if constexpr (GRADS) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = t + i * T;
-    if (c >= d8) break;
-    float v[8];
-    split8(sg[GRADS ? i : 0], v);
-    ln_put_sums(p, 0, c, v);
-    split8(sb[GRADS ? i : 0], v);
-    ln_put_sums(p, 1, c, v);
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * T;
+      if (c >= d8) break;
+      float v[8];
+      split8(sg[i], v);
+      ln_put_sums(p, 0, c, v);
+      split8(sb[i], v);
+      ln_put_sums(p, 1, c, v);
+    }
   }
 }
 
@@ -578,13 +600,15 @@ lsq_status col_sum(const float* part, int G, int64_t ld, int64_t n0, int64_t nco
 }
 
 // ---------------------------------------------------------------- geometry
-// WARP rows up to d = 1024 (V words a lane); block rows with V words a thread.  Few rows: one word a
-// thread (the row's latency decides); many: more words a thread (fewer threads per reduction).
+// WARP rows up to d = 1024 (V words a lane); block rows with V words a thread.  Few rows: one word a thread
+// (the row's latency decides).  Many: two (8192 x 5120, RMSNorm backward from a checkpoint: 53.3 / 52.2 / 59.0 us
+// with 1 / 2 / 4; restore and norm 45.8 / 35.0 / 36.0), and four where LayerNorm's two reductions a row ask for
+// fewer threads in each (46.7 / 37.8 / 32.2).
 struct Geo {
   int v, threads, warp;
   unsigned blocks;
 };
-static Geo fwd_geo(int64_t rows, int d8) {
+static Geo row_geo(int64_t rows, int d8, bool layer) {
   Geo g;
   g.warp = d8 <= 128;
   if (g.warp) {
@@ -594,7 +618,8 @@ static Geo fwd_geo(int64_t rows, int d8) {
     g.blocks = (unsigned)((rows + per - 1) / per);
     return g;
   }
-  g.v = rows >= 2 * num_sms() ? (d8 >= 512 ? 4 : d8 >= 256 ? 2 : 1) : (d8 > 1024 ? 2 : 1);
+  const bool many = rows >= 2 * num_sms();
+  g.v = d8 > 1024 ? (many ? 4 : 2) : many && d8 >= 512 && layer ? 4 : many && d8 >= 256 ? 2 : 1;
   g.threads = (((d8 + g.v - 1) / g.v) + 31) / 32 * 32;
   g.blocks = (unsigned)rows;
   return g;
@@ -626,13 +651,22 @@ static BwdGeo ln_bwd_geo(int64_t rows, int d8) {
   return g;
 }
 
+template <typename K>
+static lsq_status ring_smem(K kernel, int* configured) {
+  int dev = 0;
+  LSQ_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64 || configured[dev]) return LSQ_OK;
+  LSQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES + 1024));
+  configured[dev] = 1;
+  return LSQ_OK;
+}
 template <int SRC, int NORM, bool PACK>
 static lsq_status run_fwd(Fwd p, int64_t rows, int64_t d, const char* what, cudaStream_t s) {
   p.rows = rows;
   p.d8 = (int)(d / 8);
   p.nb = (int)((d + 63) / 64);
   p.inv_d = 1.0f / (float)d;
-  const Geo g = fwd_geo(rows, p.d8);
+  const Geo g = row_geo(rows, p.d8, NORM == LAYER);
   if (g.warp) {
     if (g.v == 1) row_fwd_kernel<1, true, SRC, NORM, PACK><<<g.blocks, g.threads, 0, s>>>(p);
     else if (g.v == 2) row_fwd_kernel<2, true, SRC, NORM, PACK><<<g.blocks, g.threads, 0, s>>>(p);
@@ -646,15 +680,6 @@ static lsq_status run_fwd(Fwd p, int64_t rows, int64_t d, const char* what, cuda
   return LSQ_OK;
 }
 
-template <typename K>
-static lsq_status ring_smem(K kernel, int* configured) {
-  int dev = 0;
-  LSQ_CUDA_TRY(cudaGetDevice(&dev));
-  if (dev < 0 || dev >= 64 || configured[dev]) return LSQ_OK;
-  LSQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES + 1024));
-  configured[dev] = 1;
-  return LSQ_OK;
-}
 template <int V, bool WARP, bool GRADS>
 static lsq_status run_ln_bwd(const Bwd& p, const BwdGeo& g, cudaStream_t s) {
   static int configured[64] = {0};
@@ -849,8 +874,8 @@ extern "C" lsq_status lsq_rmsnorm_bwd_unpack8(const void* dy, const void* ckpt, 
   p.d8 = (int)(d / 8);
   p.nb = (int)((d + 63) / 64);
   p.inv_d = 1.0f / (float)d;
-  const nrm::Geo ge = nrm::fwd_geo(rows, p.d8);
   cudaStream_t s = (cudaStream_t)stream;
+  const nrm::Geo ge = nrm::row_geo(rows, p.d8, false);
   if (ge.warp) {
     if (ge.v == 1) nrm::rms_bwd_unpack8_kernel<1, true><<<ge.blocks, ge.threads, 0, s>>>(p);
     else if (ge.v == 2) nrm::rms_bwd_unpack8_kernel<2, true><<<ge.blocks, ge.threads, 0, s>>>(p);

@@ -101,6 +101,8 @@ def args_():
                    help="lm_head resident in HBM, or in page-locked host RAM streamed in vocabulary chunks of "
                         "--head-chunk rows through two HBM buffers for each of its GEMMs")
     p.add_argument("--head-chunk", type=int, default=8192)
+    p.add_argument("--checkpoint", default="bf16", choices=["bf16", "int8"],
+                   help="layer inputs kept for the recompute: bf16, or 8-bit checkpoints")
     p.add_argument("--no-graph", action="store_true",
                    help="launch every kernel eagerly instead of replaying each step as a CUDA graph")
     p.add_argument("--absmax", default="fp32", choices=["fp32", "dq8"],
@@ -249,8 +251,9 @@ def workload_config(a, shape):
     if a.head == "host":
         emb += (f", lm_head in pinned host RAM streamed in {a.head_chunk}-row vocabulary chunks through two HBM "
                 f"buffers for each of its GEMMs")
+    ck = "grad checkpointing" if a.checkpoint == "bf16" else "grad checkpointing (8-bit layer inputs)"
     return {"workload": f"{shape.name} shape, NF4 (bs64, {am}) base streamed from {src}{emb} through "
-                        f"{a.slots} HBM slots, grad checkpointing with re-stream, LoRA r={shape.r} on all linears, "
+                        f"{a.slots} HBM slots, {ck} with re-stream, LoRA r={shape.r} on all linears, "
                         f"{task}, AdamW",
             "batch": a.batch, "seq_len": a.seq, "n_slots": a.slots, "parallelism": f"dp{a.gpus}",
             "upload": a.upload if a.upload != "auto" else ("sharded" if a.gpus > 1 else "replicated"),
@@ -382,7 +385,7 @@ def _our_arm(a):
         if a.store_path and world > 1:
             store_path = f"{a.store_path}.rank{rank}"
     tiers = dict(absmax=a.absmax, shard=shard, source=a.source, store_path=store_path, embed=a.embed, head=a.head,
-                 head_chunk=a.head_chunk, graph=graph_on(a))
+                 head_chunk=a.head_chunk, graph=graph_on(a), checkpoint=a.checkpoint)
     tr = StreamedLoraTrainer(shape, a.batch, a.seq, n_slots=a.slots, init="device", **tiers)
     ids_list = [S.tokens(shape, a.batch, a.seq, step=1000 * rank + t).cuda() for t in range(4)]
     for i in range(a.warmup):

@@ -176,13 +176,24 @@ class StreamedLoraTrainer:
     two HBM chunk buffers on the copy stream, once for each of its GEMMs (with
     a tied embedding the one host table also serves the gather, zero-copy).
     The chunked GEMMs give bit for bit the resident head's results.
+    checkpoint: "bf16" keeps every layer's input [M, d] for the recompute;
+    "int8" keeps it as an 8-bit checkpoint (1.03 bytes per element instead of
+    2), written by the layer's first norm in the forward and restored by the
+    same norm in the recompute, whose backward reads the codes again.  The
+    forward and its loss are those of "bf16" up to the norm's rounding; the
+    gradients are taken at the restored inputs, with the rank-r products
+    s*U of the forward.  The recompute leaves out the down projection, whose
+    output no backward reads.
     """
 
     def __init__(self, shape: S.ModelShape, batch: int, seq: int, n_slots: Optional[int] = 2,
                  init: str = "device", lr: float = 2e-5, device: str = "cuda", share: "StreamedLoraTrainer" = None,
                  absmax: str = "fp32", shard: Optional[tuple] = None, source: str = "ram",
                  store_path: Optional[str] = None, embed: str = "hbm", head: str = "hbm",
-                 head_chunk: int = 8192, graph: bool = False):
+                 head_chunk: int = 8192, graph: bool = False, checkpoint: str = "bf16"):
+        if checkpoint not in ("bf16", "int8"):
+            raise ValueError(f"checkpoint must be 'bf16' or 'int8', got {checkpoint!r}")
+        self.checkpoint = checkpoint
         self.shape, self.B, self.S = shape, batch, seq
         self.timeline = None   # list of (kind, flops, start_event, end_event) when instrumented
         self.M = batch * seq
@@ -355,7 +366,12 @@ class StreamedLoraTrainer:
         f32 = dict(dtype=torch.float32, device=dev)
         d, f, kv, r = sh.d, sh.f, sh.kv, sh.r
         self.ids = torch.zeros(M, dtype=torch.int32, device=dev)
-        self.h = torch.empty(sh.n_layers + 1, M, d, **bf)        # checkpointed layer inputs
+        if self.checkpoint == "int8":
+            # the running residual stream, the restored layer input, and each layer's checkpoint
+            self.h_run, self.h_in = torch.empty(M, d, **bf), torch.empty(M, d, **bf)
+            self.ckpt = torch.empty(sh.n_layers, L.lsq_ckpt8_size(M, d), dtype=torch.uint8, device=dev)
+        else:
+            self.h = torch.empty(sh.n_layers + 1, M, d, **bf)        # checkpointed layer inputs
         self.x1, self.q, self.a, self.hmid, self.x2 = (torch.empty(M, d, **bf) for _ in range(5))
         self.k, self.v = torch.empty(M, kv, **bf), torch.empty(M, kv, **bf)
         self.g, self.u, self.mm = (torch.empty(M, f, **bf) for _ in range(3))
@@ -423,6 +439,10 @@ class StreamedLoraTrainer:
         return sum(2.0 * M * n * K + 2.0 * M * n * r + 2.0 * M * r * K for n in ns)
 
     # ------------------------------------------------------------------ layer
+    def _h(self, l: int) -> torch.Tensor:
+        """The residual stream entering layer l (one running buffer with 8-bit checkpoints)."""
+        return self.h_run if self.checkpoint == "int8" else self.h[l]
+
     def _ops(self, l: int):
         lp = self.lora
         A = {n: lp.view(lp.op, l, n, "A") for n in S.LINEARS}
@@ -432,15 +452,17 @@ class StreamedLoraTrainer:
     def _layer_fwd(self, l: int, W: LayerView, save: bool, hin=None, hout=None, adapter: bool = True):
         """Layer l: hin (default h[l]) -> hout (default h[l+1], may alias hin).
         adapter=False runs the frozen base alone (r = 0): the reference model
-        of the preference loss."""
+        of the preference loss.  save: the recompute, from the layer's checkpoint."""
         sh, M = self.shape, self.M
         r, s = (sh.r, sh.s) if adapter else (0, 0.0)
         if adapter:
             A, B = self._ops(l)
         else:
             A = B = {n: None for n in S.LINEARS}
-        hin = self.h[l] if hin is None else hin
-        hout = self.h[l + 1] if hout is None else hout
+        int8 = self.checkpoint == "int8" and hin is None   # the policy's pass, not the reference's
+        if hin is None:
+            hin = self.h_in if int8 and save else self._h(l)
+        hout = self._h(l + 1) if hout is None else hout
         U = self.U if save and adapter else {n: None for n in S.LINEARS}
         state = adapter and self.keep_rank_state
         ready = save           # the recompute: the first forward of this step filled the rank state
@@ -459,7 +481,12 @@ class StreamedLoraTrainer:
                 L.lsq_nf4_lora_fwd_multi(Ws, x, M, [A[n] for n in names], [B[n] for n in names], r, s, res, ys,
                                          [U[n] for n in names], workspace=self.ws_lora)
 
-        L.lsq_rmsnorm_fwd(hin, W.ln1, self.x1, self.rstd1, M, sh.d, sh.eps)
+        if int8 and save:
+            L.lsq_rmsnorm_fwd_unpack8(self.ckpt[l], W.ln1, hin, self.x1, self.rstd1, M, sh.d, sh.eps)
+        elif int8:
+            L.lsq_rmsnorm_fwd_pack8(hin, W.ln1, self.x1, self.rstd1, self.ckpt[l], M, sh.d, sh.eps)
+        else:
+            L.lsq_rmsnorm_fwd(hin, W.ln1, self.x1, self.rstd1, M, sh.d, sh.eps)
         t = self._t0()
         rope = (self.rope_table, self.S, sh.hd, 0b011) if self.fuse_rope else None   # q and k
         fused("qkv", [W.W["q"], W.W["k"], W.W["v"]], self.x1, ["q", "k", "v"], None, [self.q, self.k, self.v], rope)
@@ -476,6 +503,8 @@ class StreamedLoraTrainer:
         fused("gateup", [W.W["gate"], W.W["up"]], self.x2, ["gate", "up"], None, [self.g, self.u])
         self._t1(t, "nf4_fwd", self._fwd_flops([sh.f, sh.f], sh.d, rf, r))
         L.lsq_swiglu_fwd(self.g, self.u, self.mm, M * sh.f)
+        if int8 and save and state:
+            return                 # the backward reads mm and the rank state, not the down projection's output
         t = self._t0()
         fused("down", [W.W["down"]], self.mm, ["down"], [self.hmid], [hout])
         self._t1(t, "nf4_fwd", self._fwd_flops([sh.d], sh.f, rf, r))
@@ -522,7 +551,10 @@ class StreamedLoraTrainer:
         fused_bwd("qkv", [W.W["q"], W.W["k"], W.W["v"]], self.x1, [self.dq, self.dk, self.dv], ["q", "k", "v"],
                   self.dx)
         self._t1(t, "nf4_bwd", self._bwd_flops([sh.d, sh.kv, sh.kv], sh.d))
-        L.lsq_rmsnorm_bwd(self.dx, self.h[l], W.ln1, self.rstd1, self.dhmid, self.dh, M, sh.d)
+        if self.checkpoint == "int8":
+            L.lsq_rmsnorm_bwd_unpack8(self.dx, self.ckpt[l], W.ln1, self.rstd1, self.dhmid, self.dh, M, sh.d)
+        else:
+            L.lsq_rmsnorm_bwd(self.dx, self.h[l], W.ln1, self.rstd1, self.dhmid, self.dh, M, sh.d)
 
     def _head_chunk_rows(self, c: int):
         r0 = c * self.head_chunk
@@ -635,15 +667,15 @@ class StreamedLoraTrainer:
 
     def _forward_backward(self):
         sh, M = self.shape, self.M
-        L.lsq_embed_gather(self.ids, self.embed, self.h[0], M, sh.d, sh.vocab)
+        L.lsq_embed_gather(self.ids, self.embed, self._h(0), M, sh.d, sh.vocab)
         for l in range(sh.n_layers):
             self._layer_fwd(l, self._view(l, +1), save=False)
-        L.lsq_rmsnorm_fwd(self.h[sh.n_layers], self.final_norm, self.hn, self.rstdf, M, sh.d, sh.eps)
+        L.lsq_rmsnorm_fwd(self._h(sh.n_layers), self.final_norm, self.hn, self.rstdf, M, sh.d, sh.eps)
         self._head_logits()
         L.lsq_xent_fwd_bwd(self.logits, self.ids, self.B, self.S, sh.vocab, self.loss_dev, self.dlogits,
                            self.ws_xent)
         self._head_dh()   # hn <- d hn
-        L.lsq_rmsnorm_bwd(self.hn, self.h[sh.n_layers], self.final_norm, self.rstdf, None, self.dh, M, sh.d)
+        L.lsq_rmsnorm_bwd(self.hn, self._h(sh.n_layers), self.final_norm, self.rstdf, None, self.dh, M, sh.d)
         for l in reversed(range(sh.n_layers)):
             W = self._view(l, -1)
             self._layer_fwd(l, W, save=True)
@@ -651,7 +683,7 @@ class StreamedLoraTrainer:
 
     def _dpo_buffers(self):
         if getattr(self, "h_ref", None) is None:
-            dev, M = self.h.device, self.M
+            dev, M = self.x1.device, self.M
             self.h_ref = torch.empty(M, self.shape.d, dtype=torch.bfloat16, device=dev)
             self.row_lse = torch.empty(M, dtype=torch.float32, device=dev)
             self.pi_logp, self.ref_logp, self.dseq = (torch.empty(self.B, dtype=torch.float32, device=dev)
@@ -676,7 +708,7 @@ class StreamedLoraTrainer:
         if self.B % 2:
             raise ValueError("DPO needs an even batch (pairs of chosen / rejected sequences)")
         self._dpo_buffers()
-        L.lsq_embed_gather(self.ids, self.embed, self.h[0], M, sh.d, sh.vocab)
+        L.lsq_embed_gather(self.ids, self.embed, self._h(0), M, sh.d, sh.vocab)
         L.lsq_embed_gather(self.ids, self.embed, self.h_ref, M, sh.d, sh.vocab)
         for l in range(sh.n_layers):
             W = self._view(l, +1)
@@ -687,14 +719,14 @@ class StreamedLoraTrainer:
         self._head_logits()
         L.lsq_seq_logprob(self.logits, self.ids, self.B, self.S, sh.vocab, self.row_lse, self.ref_logp, self.ws_seqlp)
         # policy sequence log-probabilities, loss, d loss / d logits
-        L.lsq_rmsnorm_fwd(self.h[sh.n_layers], self.final_norm, self.hn, self.rstdf, M, sh.d, sh.eps)
+        L.lsq_rmsnorm_fwd(self._h(sh.n_layers), self.final_norm, self.hn, self.rstdf, M, sh.d, sh.eps)
         self._head_logits()
         L.lsq_seq_logprob(self.logits, self.ids, self.B, self.S, sh.vocab, self.row_lse, self.pi_logp, self.ws_seqlp)
         L.lsq_dpo_loss(self.pi_logp, self.ref_logp, self.B // 2, beta, self.loss_dev, self.dseq)
         L.lsq_seq_logprob_bwd(self.logits, self.ids, self.B, self.S, sh.vocab, self.row_lse, self.dseq,
                               self.dlogits)
         self._head_dh()   # hn <- d hn
-        L.lsq_rmsnorm_bwd(self.hn, self.h[sh.n_layers], self.final_norm, self.rstdf, None, self.dh, M, sh.d)
+        L.lsq_rmsnorm_bwd(self.hn, self._h(sh.n_layers), self.final_norm, self.rstdf, None, self.dh, M, sh.d)
         for l in reversed(range(sh.n_layers)):
             W = self._view(l, -1)
             self._layer_fwd(l, W, save=True)

@@ -89,6 +89,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int wh
   }
 }
 
+// ---------------------------------------------------------------- programmatic launch
+// A kernel launched by launch_chained (host_common.h) may start while its predecessor on the stream still
+// runs: it sets up (shared memory, barriers, tensor memory), calls grid_wait before its first access to global
+// memory, which returns once the predecessor has finished and its writes are visible, and calls grid_release
+// so that its own successor may do the same.  Every thread that touches global memory calls grid_wait.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- proxies
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

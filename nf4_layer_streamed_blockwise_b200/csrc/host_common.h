@@ -33,6 +33,28 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 int num_sms();
 
+// Launch with programmatic stream serialization (and a cluster size, where above 1): the kernel may be set up
+// while its predecessor on the stream still runs, so it must call grid_wait (common.cuh).
+template <typename... P, typename... A>
+lsq_status launch_chained(const char* what, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+                          unsigned cluster, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  return e == cudaSuccess ? LSQ_OK : cuda_fail(e, what);
+}
+
 }  // namespace lsq
 
 #define LSQ_CUDA_TRY(call)                                        \

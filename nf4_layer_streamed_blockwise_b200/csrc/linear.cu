@@ -252,6 +252,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  grid_release();
+  grid_wait();
   // the cluster's CTAs have started once this phase completes (waited for before the exchange)
   if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
@@ -425,6 +427,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GTHREADS, 1)
   nf4g::cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  grid_release();
+  grid_wait();
 
   if (warp == 8) {
     const int hb = p.bn / 2, nbox = (hb + 63) / 64;  // this CTA's columns; 64-wide boxes of an MN-major P
@@ -612,9 +616,8 @@ static lsq_status launch_pair(const GMaps& maps, const Params& p, int64_t tiles,
     configured[dev] = 1;
   }
   const unsigned ncl = (unsigned)std::min<int64_t>(tiles, num_sms() / 2);
-  linear_pair_kernel<AMN, BMN, F32><<<2 * ncl, GTHREADS, G_BYTES, stream>>>(maps, p);
-  LSQ_LAUNCH_CHECK("linear_pair_kernel");
-  return LSQ_OK;
+  return launch_chained("linear_pair_kernel", linear_pair_kernel<AMN, BMN, F32>, dim3(2 * ncl), GTHREADS, G_BYTES, 1,
+                        stream, maps, p);
 }
 
 // K-major operand [rows, C] with box {64, brows}; MN-major operand [C, rows] with box {64, 64}
@@ -635,20 +638,8 @@ static lsq_status launch_split(const Maps& maps, const Params& p, int64_t cluste
                                       Cfg<BT>::BYTES));
     configured[dev] = 1;
   }
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)(clusters * p.splits));
-  cfg.blockDim = dim3(NTHREADS);
-  cfg.dynamicSmemBytes = Cfg<BT>::BYTES;
-  cfg.stream = stream;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)p.splits;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  LSQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_split_kernel<PMN, QMN, BT>, maps, p));
-  return LSQ_OK;
+  return launch_chained("linear_split_kernel", linear_split_kernel<PMN, QMN, BT>, dim3((unsigned)(clusters * p.splits)),
+                        NTHREADS, Cfg<BT>::BYTES, (unsigned)p.splits, stream, maps, p);
 }
 
 // Which form a product takes, and its tile: the smallest estimate in us, from measurements of both forms on
@@ -747,7 +738,8 @@ __global__ void __launch_bounds__(256, 4) dz_kernel(const uint4* __restrict__ dy
                                                  uint4* __restrict__ dz, float* __restrict__ part, int64_t rows, int n8,
                                                  int64_t strip) {
   __shared__ float comb[8][32][9];
-  nrm::grid_release();
+  grid_release();
+  grid_wait();
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + l;
   const int64_t r0 = blockIdx.y * strip, r1 = r0 + strip < rows ? r0 + strip : rows;
@@ -863,17 +855,15 @@ extern "C" lsq_status lsq_linear_bwd(const void* dy, const void* x, const void* 
     const int64_t strips = lin::strips_of(M, N), strip = (M + strips - 1) / strips;
     const int ns = (int)((M + strip - 1) / strip);
     const dim3 grid((unsigned)((N + 255) / 256), (unsigned)ns);
-    const uint4 *a = (const uint4*)dy, *b = (const uint4*)z;
-    uint4* o = (uint4*)dz;
     const int n8 = (int)(N / 8);
-    switch (act) {
-      case LSQ_ACT_RELU: lin::dz_kernel<LSQ_ACT_RELU><<<grid, 256, 0, s>>>(a, b, o, part, M, n8, strip); break;
-      case LSQ_ACT_GELU: lin::dz_kernel<LSQ_ACT_GELU><<<grid, 256, 0, s>>>(a, b, o, part, M, n8, strip); break;
-      case LSQ_ACT_GELU_TANH: lin::dz_kernel<LSQ_ACT_GELU_TANH><<<grid, 256, 0, s>>>(a, b, o, part, M, n8, strip); break;
-      case LSQ_ACT_SILU: lin::dz_kernel<LSQ_ACT_SILU><<<grid, 256, 0, s>>>(a, b, o, part, M, n8, strip); break;
-      default: lin::dz_kernel<LSQ_ACT_NONE><<<grid, 256, 0, s>>>(a, b, nullptr, part, M, n8, strip); break;
-    }
-    LSQ_LAUNCH_CHECK("dz_kernel");
+    auto k = act == LSQ_ACT_RELU        ? lin::dz_kernel<LSQ_ACT_RELU>
+             : act == LSQ_ACT_GELU      ? lin::dz_kernel<LSQ_ACT_GELU>
+             : act == LSQ_ACT_GELU_TANH ? lin::dz_kernel<LSQ_ACT_GELU_TANH>
+             : act == LSQ_ACT_SILU      ? lin::dz_kernel<LSQ_ACT_SILU>
+                                        : lin::dz_kernel<LSQ_ACT_NONE>;
+    st = launch_chained("dz_kernel", k, grid, 256, 0, 1, s, (const uint4*)dy, (const uint4*)z,
+                        act == LSQ_ACT_NONE ? (uint4*)nullptr : (uint4*)const_cast<void*>(dz), part, M, n8, strip);
+    if (st != LSQ_OK) return st;
     if (dbias && (st = nrm::col_sum(part, ns, N, N, N, dbias, nullptr, accumulate ? 1 : 0, s)) != LSQ_OK) return st;
   }
   if (dx) {

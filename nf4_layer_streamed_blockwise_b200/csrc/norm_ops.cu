@@ -21,11 +21,6 @@ constexpr int64_t MAX_D = 16384;  // 2048 words: 512 threads x 4, or 1024 x 2
 enum { NONE = 0, RMS = 1, LAYER = 2 };
 enum { BF16 = 0, CKPT8 = 1 };
 
-// Programmatic launch: a kernel that called grid_release lets a dependent launch start early; the dependent's
-// grid_wait returns once that kernel has finished and its writes are visible.
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -139,6 +134,8 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) row_fwd_kern
   const int T = WARP ? 32 : (int)blockDim.x;
   const int t = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
   const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  grid_release();
+  grid_wait();
   if (WARP && row >= p.rows) return;  // whole warps; no block barrier follows
   const int d8 = p.d8;
   const int64_t base = row * d8, bbase = row * p.nb;
@@ -261,6 +258,8 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) rms_bwd_unpa
   const int T = WARP ? 32 : (int)blockDim.x;
   const int t = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
   const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  grid_release();
+  grid_wait();
   if (WARP && row >= p.rows) return;
   const int d8 = p.d8;
   const int64_t base = row * d8, bbase = row * p.nb;
@@ -379,7 +378,6 @@ constexpr int LNW = 8;
 template <int V, bool GRADS>
 __global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_constant__ Bwd p, int nst, int stage) {
   extern __shared__ __align__(128) uint8_t smem[];  // per warp [nst][x | dy | res], then every stage's barrier
-  if (GRADS) grid_release();
   __shared__ float comb[LNW * 32 * 9];
   const int t = (int)(threadIdx.x & 31), w = (int)(threadIdx.x >> 5);
   uint8_t* ring = smem + (size_t)w * nst * stage;
@@ -391,9 +389,12 @@ __global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_c
   if (t == 0) {
     for (int s = 0; s < nst; ++s) mbar_init(&full[s], 1);
     fence_barrier_init();
+  }
+  grid_release();
+  grid_wait();
+  if (t == 0)
     for (int s = 0; s < nst; ++s)
       if (first + s * step < p.rows) ln_fetch(p, ring + (size_t)s * stage, &full[s], rb, first + s * step);
-  }
   __syncwarp();
   uint4 gv[V];
   uint64_t sg[GRADS ? V : 1][4], sb[GRADS ? V : 1][4];
@@ -461,7 +462,6 @@ template <int V, bool GRADS>
 __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
     ln_bwd_block_kernel(const __grid_constant__ Bwd p, int nst, int stage) {
   extern __shared__ __align__(128) uint8_t ring[];  // [nst][x | dy | res], then the stages' barriers
-  if (GRADS) grid_release();
   __shared__ float2 red[2][16];
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)nst * stage);
   const int T = (int)blockDim.x, t = (int)threadIdx.x, d8 = p.d8, nw = T >> 5, lane = t & 31;
@@ -471,9 +471,12 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
   if (t == 0) {
     for (int s = 0; s < nst; ++s) mbar_init(&full[s], 1);
     fence_barrier_init();
+  }
+  grid_release();
+  grid_wait();
+  if (t == 0)
     for (int s = 0; s < nst; ++s)
       if (first + s * step < p.rows) ln_fetch(p, ring + (size_t)s * stage, &full[s], rb, first + s * step);
-  }
   __syncthreads();
   uint64_t sg[GRADS ? V : 1][4], sb[GRADS ? V : 1][4];
   uint4 gv[V];
@@ -546,7 +549,8 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
 __global__ void __launch_bounds__(1024) col_sum_kernel(const float* __restrict__ part, int G, int64_t ld, int64_t n0,
                                                        int64_t ncols, float* out0, float* out1, int accumulate) {
   __shared__ float2 s[32][33];
-  grid_wait();  // launched while the kernel that writes part still runs
+  grid_release();
+  grid_wait();
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   const int64_t c = ((int64_t)blockIdx.x * 32 + l) * 2;
   float2 v = make_float2(0.0f, 0.0f);
@@ -584,19 +588,8 @@ __global__ void __launch_bounds__(1024) col_sum_kernel(const float* __restrict__
 
 lsq_status col_sum(const float* part, int G, int64_t ld, int64_t n0, int64_t ncols, float* out0, float* out1,
                    int accumulate, cudaStream_t stream) {
-  // programmatic launch: its blocks are set up behind the running kernel's, 4 -> 2 us for a short sum
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)((ncols + 63) / 64));
-  cfg.blockDim = dim3(1024);
-  cfg.stream = stream;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  LSQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, col_sum_kernel, part, G, ld, n0, ncols, out0, out1, accumulate));
-  return LSQ_OK;
+  return launch_chained("col_sum_kernel", col_sum_kernel, dim3((unsigned)((ncols + 63) / 64)), 1024, 0, 1, stream, part,
+                        G, ld, n0, ncols, out0, out1, accumulate);
 }
 
 // ---------------------------------------------------------------- geometry
@@ -667,19 +660,14 @@ static lsq_status run_fwd(Fwd p, int64_t rows, int64_t d, const char* what, cuda
   p.nb = (int)((d + 63) / 64);
   p.inv_d = 1.0f / (float)d;
   const Geo g = row_geo(rows, p.d8, NORM == LAYER);
-  if (g.warp) {
-    if (g.v == 1) row_fwd_kernel<1, true, SRC, NORM, PACK><<<g.blocks, g.threads, 0, s>>>(p);
-    else if (g.v == 2) row_fwd_kernel<2, true, SRC, NORM, PACK><<<g.blocks, g.threads, 0, s>>>(p);
-    else row_fwd_kernel<4, true, SRC, NORM, PACK><<<g.blocks, g.threads, 0, s>>>(p);
-  } else {
-    if (g.v == 1) row_fwd_kernel<1, false, SRC, NORM, PACK><<<g.blocks, g.threads, 0, s>>>(p);
-    else if (g.v == 2) row_fwd_kernel<2, false, SRC, NORM, PACK><<<g.blocks, g.threads, 0, s>>>(p);
-    else row_fwd_kernel<4, false, SRC, NORM, PACK><<<g.blocks, g.threads, 0, s>>>(p);
-  }
-  LSQ_LAUNCH_CHECK(what);
-  return LSQ_OK;
+  auto k = g.warp ? (g.v == 1   ? row_fwd_kernel<1, true, SRC, NORM, PACK>
+                     : g.v == 2 ? row_fwd_kernel<2, true, SRC, NORM, PACK>
+                                : row_fwd_kernel<4, true, SRC, NORM, PACK>)
+                  : (g.v == 1   ? row_fwd_kernel<1, false, SRC, NORM, PACK>
+                     : g.v == 2 ? row_fwd_kernel<2, false, SRC, NORM, PACK>
+                                : row_fwd_kernel<4, false, SRC, NORM, PACK>);
+  return launch_chained(what, k, dim3(g.blocks), (unsigned)g.threads, 0, 1, s, p);
 }
-
 template <int V, bool WARP, bool GRADS>
 static lsq_status run_ln_bwd(const Bwd& p, const BwdGeo& g, cudaStream_t s) {
   static int configured[64] = {0};
@@ -687,14 +675,14 @@ static lsq_status run_ln_bwd(const Bwd& p, const BwdGeo& g, cudaStream_t s) {
   if constexpr (WARP) {
     lsq_status st = ring_smem(ln_bwd_warp_kernel<V, GRADS>, configured);
     if (st != LSQ_OK) return st;
-    ln_bwd_warp_kernel<V, GRADS><<<g.blocks, g.threads, smem, s>>>(p, g.nst, g.stage);
+    return launch_chained("ln_bwd_warp_kernel", ln_bwd_warp_kernel<V, GRADS>, dim3(g.blocks), (unsigned)g.threads, smem,
+                          1, s, p, g.nst, g.stage);
   } else {
     lsq_status st = ring_smem(ln_bwd_block_kernel<V, GRADS>, configured);
     if (st != LSQ_OK) return st;
-    ln_bwd_block_kernel<V, GRADS><<<g.blocks, g.threads, smem, s>>>(p, g.nst, g.stage);
+    return launch_chained("ln_bwd_block_kernel", ln_bwd_block_kernel<V, GRADS>, dim3(g.blocks), (unsigned)g.threads,
+                          smem, 1, s, p, g.nst, g.stage);
   }
-  LSQ_LAUNCH_CHECK("ln_bwd kernel");
-  return LSQ_OK;
 }
 template <int V, bool WARP>
 static lsq_status run_ln_bwd(const Bwd& p, bool grads, const BwdGeo& g, cudaStream_t s) {
@@ -876,15 +864,11 @@ extern "C" lsq_status lsq_rmsnorm_bwd_unpack8(const void* dy, const void* ckpt, 
   p.inv_d = 1.0f / (float)d;
   cudaStream_t s = (cudaStream_t)stream;
   const nrm::Geo ge = nrm::row_geo(rows, p.d8, false);
-  if (ge.warp) {
-    if (ge.v == 1) nrm::rms_bwd_unpack8_kernel<1, true><<<ge.blocks, ge.threads, 0, s>>>(p);
-    else if (ge.v == 2) nrm::rms_bwd_unpack8_kernel<2, true><<<ge.blocks, ge.threads, 0, s>>>(p);
-    else nrm::rms_bwd_unpack8_kernel<4, true><<<ge.blocks, ge.threads, 0, s>>>(p);
-  } else {
-    if (ge.v == 1) nrm::rms_bwd_unpack8_kernel<1, false><<<ge.blocks, ge.threads, 0, s>>>(p);
-    else if (ge.v == 2) nrm::rms_bwd_unpack8_kernel<2, false><<<ge.blocks, ge.threads, 0, s>>>(p);
-    else nrm::rms_bwd_unpack8_kernel<4, false><<<ge.blocks, ge.threads, 0, s>>>(p);
-  }
-  LSQ_LAUNCH_CHECK("rms_bwd_unpack8_kernel");
-  return LSQ_OK;
+  auto k = ge.warp ? (ge.v == 1   ? nrm::rms_bwd_unpack8_kernel<1, true>
+                      : ge.v == 2 ? nrm::rms_bwd_unpack8_kernel<2, true>
+                                  : nrm::rms_bwd_unpack8_kernel<4, true>)
+                   : (ge.v == 1   ? nrm::rms_bwd_unpack8_kernel<1, false>
+                      : ge.v == 2 ? nrm::rms_bwd_unpack8_kernel<2, false>
+                                  : nrm::rms_bwd_unpack8_kernel<4, false>);
+  return launch_chained("rms_bwd_unpack8_kernel", k, dim3(ge.blocks), (unsigned)ge.threads, 0, 1, s, p);
 }

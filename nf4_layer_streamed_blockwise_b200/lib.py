@@ -223,7 +223,9 @@ _KERNELS = {"lsq_nf4_quantize": 1, "lsq_nf4_dequantize": 1, "lsq_absmax_double_q
 
 
 def _call(name, *args, launches=None):
-    _check(name, _fn(name)(*args))
+    status = (_FNS.get(name) or _fn(name))(*args)
+    if status:
+        _check(name, status)
     LAUNCHES[0] += _KERNELS.get(name, 0) if launches is None else launches
 
 
@@ -586,11 +588,10 @@ def _t(fn: str, name: str, t, dtype, n: int, dev: int) -> Optional[int]:
     if t is None or t.__class__ is int:
         return t
     if dtype is None:
-        if t.numel() * t.element_size() < n:
-            _bad(fn, name, t, dtype, n)
-    elif t.dtype is not dtype or t.numel() < n:
-        _bad(fn, name, t, dtype, n)
-    if not t.is_contiguous() or t.get_device() != dev:
+        short = t.numel() * t.element_size() < n
+    else:
+        short = t.dtype is not dtype or t.numel() < n
+    if short or not t.is_contiguous() or t.get_device() != dev:
         _bad(fn, name, t, dtype, n)
     return t.data_ptr()
 
@@ -615,8 +616,8 @@ def lsq_layernorm_bwd(dy, x, g, mean, rstd, dres_in, dres_out, dg, db, accumulat
                       stream=None):
     """dres_out = dres_in + dx; dg, db fp32 (None: frozen), overwritten or (accumulate=1) added to."""
     f, dev, n, bf, f32 = "lsq_layernorm_bwd", _dev(), rows * d, torch.bfloat16, torch.float32
-    # the rows of one block (16 of at most 1024 columns; fewer of longer rows) need no second kernel
-    two = (dg is not None or db is not None) and lsq_layernorm_bwd_workspace_size(rows, d) > -(-8 * d // 256) * 256
+    # the rows of one block (8 of at most 768 columns, else one) need no second kernel
+    two = (dg is not None or db is not None) and rows > (8 if d <= 768 else 1)
     _call(f, _t(f, "dy", dy, bf, n, dev), _t(f, "x", x, bf, n, dev), _t(f, "g", g, bf, d, dev),
           _t(f, "mean", mean, f32, rows, dev), _t(f, "rstd", rstd, f32, rows, dev),
           _t(f, "dres_in", dres_in, bf, n, dev), _t(f, "dres_out", dres_out, bf, n, dev), _t(f, "dg", dg, f32, d, dev),
@@ -629,15 +630,20 @@ def lsq_ckpt8_size(rows: int, d: int) -> int:
     return int(_fn("lsq_ckpt8_size")(rows, d))
 
 
+def _ckpt8_used(rows: int, d: int) -> int:
+    """The bytes of a checkpoint that are read and written (layout: include/lsq.h)."""
+    return (rows * d + 15) // 16 * 16 + 2 * rows * ((d + 63) // 64)
+
+
 def lsq_ckpt8_pack(x, ckpt, rows: int, d: int, stream=None):
     f, dev = "lsq_ckpt8_pack", _dev()
-    _call(f, _t(f, "x", x, torch.bfloat16, rows * d, dev), _t(f, "ckpt", ckpt, None, lsq_ckpt8_size(rows, d), dev),
+    _call(f, _t(f, "x", x, torch.bfloat16, rows * d, dev), _t(f, "ckpt", ckpt, None, _ckpt8_used(rows, d), dev),
           rows, d, _stream(stream))
 
 
 def lsq_ckpt8_unpack(ckpt, x, rows: int, d: int, stream=None):
     f, dev = "lsq_ckpt8_unpack", _dev()
-    _call(f, _t(f, "ckpt", ckpt, None, lsq_ckpt8_size(rows, d), dev), _t(f, "x", x, torch.bfloat16, rows * d, dev),
+    _call(f, _t(f, "ckpt", ckpt, None, _ckpt8_used(rows, d), dev), _t(f, "x", x, torch.bfloat16, rows * d, dev),
           rows, d, _stream(stream))
 
 
@@ -645,14 +651,14 @@ def lsq_rmsnorm_fwd_pack8(x, g, y, rstd, ckpt, rows: int, d: int, eps: float, st
     """lsq_rmsnorm_fwd that also leaves x's 8-bit checkpoint."""
     f, dev, n, bf = "lsq_rmsnorm_fwd_pack8", _dev(), rows * d, torch.bfloat16
     _call(f, _t(f, "x", x, bf, n, dev), _t(f, "g", g, bf, d, dev), _t(f, "y", y, bf, n, dev),
-          _t(f, "rstd", rstd, torch.float32, rows, dev), _t(f, "ckpt", ckpt, None, lsq_ckpt8_size(rows, d), dev),
+          _t(f, "rstd", rstd, torch.float32, rows, dev), _t(f, "ckpt", ckpt, None, _ckpt8_used(rows, d), dev),
           rows, d, eps, _stream(stream))
 
 
 def lsq_rmsnorm_fwd_unpack8(ckpt, g, x, y, rstd, rows: int, d: int, eps: float, stream=None):
     """x restored from its 8-bit checkpoint, and lsq_rmsnorm_fwd of it."""
     f, dev, n, bf = "lsq_rmsnorm_fwd_unpack8", _dev(), rows * d, torch.bfloat16
-    _call(f, _t(f, "ckpt", ckpt, None, lsq_ckpt8_size(rows, d), dev), _t(f, "g", g, bf, d, dev),
+    _call(f, _t(f, "ckpt", ckpt, None, _ckpt8_used(rows, d), dev), _t(f, "g", g, bf, d, dev),
           _t(f, "x", x, bf, n, dev), _t(f, "y", y, bf, n, dev), _t(f, "rstd", rstd, torch.float32, rows, dev), rows, d,
           eps, _stream(stream))
 
@@ -660,7 +666,7 @@ def lsq_rmsnorm_fwd_unpack8(ckpt, g, x, y, rstd, rows: int, d: int, eps: float, 
 def lsq_rmsnorm_bwd_unpack8(dy, ckpt, g, rstd, dres_in, dres_out, rows: int, d: int, stream=None):
     """lsq_rmsnorm_bwd with x read from its 8-bit checkpoint."""
     f, dev, n, bf = "lsq_rmsnorm_bwd_unpack8", _dev(), rows * d, torch.bfloat16
-    _call(f, _t(f, "dy", dy, bf, n, dev), _t(f, "ckpt", ckpt, None, lsq_ckpt8_size(rows, d), dev),
+    _call(f, _t(f, "dy", dy, bf, n, dev), _t(f, "ckpt", ckpt, None, _ckpt8_used(rows, d), dev),
           _t(f, "g", g, bf, d, dev), _t(f, "rstd", rstd, torch.float32, rows, dev),
           _t(f, "dres_in", dres_in, bf, n, dev), _t(f, "dres_out", dres_out, bf, n, dev), rows, d, _stream(stream))
 

@@ -85,24 +85,29 @@ __device__ __forceinline__ uint32_t block_amax(uint4 w) {
 __device__ __forceinline__ uint2 encode8(uint4 w, uint32_t amax) {
   if (amax == 0u || amax == 0x7fc0u) return make_uint2(0u, 0u);
   const float inv = CODE_GAIN / __uint_as_float(amax << 16);
-  float f[8];
-  unpack8(w, f);
+  uint64_t f[4];
+  unpack_pairs(w, f);
   uint32_t u[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(fmaf(f[i], inv, CODE_MAGIC));
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t v = fma2(f[i], f2(inv, inv), f2(CODE_MAGIC, CODE_MAGIC));
+    u[2 * i] = (uint32_t)v;
+    u[2 * i + 1] = (uint32_t)(v >> 32);
+  }
   return make_uint2(__byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410),
                     __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410));
 }
 __device__ __forceinline__ uint4 decode8(uint2 codes, uint32_t amax) {
   const float s = __uint_as_float(amax << 16) * INV_127;
-  float f[8];
+  uint64_t f[4];
   const uint32_t a = codes.x ^ 0x80808080u, b = codes.y ^ 0x80808080u;  // q + 128, unsigned
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = (__uint_as_float(__byte_perm(a, 0x4b000000u, 0x7440 + i)) - 8388736.0f) * s;  // 2^23 + q + 128
-    f[4 + i] = (__uint_as_float(__byte_perm(b, 0x4b000000u, 0x7440 + i)) - 8388736.0f) * s;
+  for (int i = 0; i < 4; ++i) {  // 2^23 + q + 128 as a float, two a step
+    const uint32_t c = i < 2 ? a : b, at = 0x7440 + 2 * (i & 1);
+    const uint64_t v = (uint64_t)__byte_perm(c, 0x4b000000u, at) | (uint64_t)__byte_perm(c, 0x4b000000u, at + 1) << 32;
+    f[i] = mul2(add2(v, f2(-8388736.0f, -8388736.0f)), f2(s, s));
   }
-  return pack8(f);
+  return pack_pairs(f);
 }
 
 struct Ckpt {
@@ -213,26 +218,26 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) row_fwd_kern
     }
   }
   if constexpr (NORM == RMS) {
-    float ss = 0.0f;
+    uint64_t acc = 0ull;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float f[8];
-      unpack8(xv[i], f);
+      uint64_t f[4];
+      unpack_pairs(xv[i], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+      for (int j = 0; j < 4; ++j) acc = fma2(f[j], f[j], acc);
     }
-    const float rs = 1.0f / sqrtf(row_sum<WARP>(ss, red[0]) * p.inv_d + p.eps);
+    const float rs = 1.0f / sqrtf(row_sum<WARP>(pair_sum(acc), red[0]) * p.inv_d + p.eps);
     if (t == 0 && p.rstd) p.rstd[row] = rs;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = t + i * T;
       if (c >= d8) break;
-      float f[8], gv[8];
-      unpack8(xv[i], f);
-      unpack8(p.g[c], gv);
+      uint64_t f[4], g[4];
+      unpack_pairs(xv[i], f);
+      unpack_pairs(p.g[c], g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = f[j] * rs * gv[j];
-      p.y[base + c] = pack8(f);
+      for (int j = 0; j < 4; ++j) f[j] = mul2(mul2(f[j], f2(rs, rs)), g[j]);
+      p.y[base + c] = pack_pairs(f);
     }
   }
 }
@@ -594,14 +599,15 @@ lsq_status col_sum(const float* part, int G, int64_t ld, int64_t n0, int64_t nco
 
 // ---------------------------------------------------------------- geometry
 // WARP rows up to d = 1024 (V words a lane); block rows with V words a thread.  Few rows: one word a thread
-// (the row's latency decides).  Many: two (8192 x 5120, RMSNorm backward from a checkpoint: 53.3 / 52.2 / 59.0 us
-// with 1 / 2 / 4; restore and norm 45.8 / 35.0 / 36.0), and four where LayerNorm's two reductions a row ask for
-// fewer threads in each (46.7 / 37.8 / 32.2).
+// (the row's latency decides).  Many, for 8192 x 5120 with 1 / 2 / 4 words: norm and checkpoint 46.7 / 35.0 /
+// 36.4 us, restore and norm 42.7 / 34.2 / 34.9; LayerNorm's two reductions a row ask for fewer threads in each
+// (46.7 / 37.8 / 31.7), the backward's three arrays for fewer registers (50.8 / 57.9 / 60.3).
+enum Pass { FORWARD, LAYERNORM, BACKWARD };
 struct Geo {
   int v, threads, warp;
   unsigned blocks;
 };
-static Geo row_geo(int64_t rows, int d8, bool layer) {
+static Geo row_geo(int64_t rows, int d8, Pass pass) {
   Geo g;
   g.warp = d8 <= 128;
   if (g.warp) {
@@ -611,8 +617,8 @@ static Geo row_geo(int64_t rows, int d8, bool layer) {
     g.blocks = (unsigned)((rows + per - 1) / per);
     return g;
   }
-  const bool many = rows >= 2 * num_sms();
-  g.v = d8 > 1024 ? (many ? 4 : 2) : many && d8 >= 512 && layer ? 4 : many && d8 >= 256 ? 2 : 1;
+  const bool many = rows >= 2 * num_sms() && pass != BACKWARD;
+  g.v = d8 > 1024 ? (many ? 4 : 2) : many && d8 >= 512 && pass == LAYERNORM ? 4 : many && d8 >= 256 ? 2 : 1;
   g.threads = (((d8 + g.v - 1) / g.v) + 31) / 32 * 32;
   g.blocks = (unsigned)rows;
   return g;
@@ -659,7 +665,7 @@ static lsq_status run_fwd(Fwd p, int64_t rows, int64_t d, const char* what, cuda
   p.d8 = (int)(d / 8);
   p.nb = (int)((d + 63) / 64);
   p.inv_d = 1.0f / (float)d;
-  const Geo g = row_geo(rows, p.d8, NORM == LAYER);
+  const Geo g = row_geo(rows, p.d8, NORM == LAYER ? LAYERNORM : FORWARD);
   auto k = g.warp ? (g.v == 1   ? row_fwd_kernel<1, true, SRC, NORM, PACK>
                      : g.v == 2 ? row_fwd_kernel<2, true, SRC, NORM, PACK>
                                 : row_fwd_kernel<4, true, SRC, NORM, PACK>)
@@ -863,12 +869,10 @@ extern "C" lsq_status lsq_rmsnorm_bwd_unpack8(const void* dy, const void* ckpt, 
   p.nb = (int)((d + 63) / 64);
   p.inv_d = 1.0f / (float)d;
   cudaStream_t s = (cudaStream_t)stream;
-  const nrm::Geo ge = nrm::row_geo(rows, p.d8, false);
+  const nrm::Geo ge = nrm::row_geo(rows, p.d8, nrm::BACKWARD);
   auto k = ge.warp ? (ge.v == 1   ? nrm::rms_bwd_unpack8_kernel<1, true>
                       : ge.v == 2 ? nrm::rms_bwd_unpack8_kernel<2, true>
                                   : nrm::rms_bwd_unpack8_kernel<4, true>)
-                   : (ge.v == 1   ? nrm::rms_bwd_unpack8_kernel<1, false>
-                      : ge.v == 2 ? nrm::rms_bwd_unpack8_kernel<2, false>
-                                  : nrm::rms_bwd_unpack8_kernel<4, false>);
+                   : (ge.v == 1 ? nrm::rms_bwd_unpack8_kernel<1, false> : nrm::rms_bwd_unpack8_kernel<2, false>);
   return launch_chained("rms_bwd_unpack8_kernel", k, dim3(ge.blocks), (unsigned)ge.threads, 0, 1, s, p);
 }

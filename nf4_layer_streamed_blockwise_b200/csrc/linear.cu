@@ -10,6 +10,15 @@
 //   forward  p = n, q = m, c = k:  P = W  K-major,   Q = x  K-major
 //   dx       p = k, q = m, c = n:  P = W  MN-major,  Q = dz K-major
 //   dW       p = k, q = n, c = m:  P = x  MN-major,  Q = dz MN-major
+//
+// Two forms share them: one tile per cluster with the contraction split (few
+// tiles: bound by what L2 feeds an SM, and below that by start and exchange)
+// and a persistent CTA-pair form (many tiles: bound by the tensor cores, in a
+// long run by the power cap); plan_product picks by a measured cost model.
+// Measured on B200 (graph replays): 2048 x 14336 x 4096 forward 153-156 us with
+// any activation (1.55 PFLOP/s; 138 us and 86% of the tensor pipe in isolation
+// at full clock), 188 with bias, residual and z kept, dx 165, dW 166;
+// 333 x 1536 x 576 6.0; 1 x 4096 x 4096 7.0 (8.7 a call with the weight from HBM).
 #include <algorithm>
 #include <cmath>
 
@@ -312,8 +321,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_
     if (ok) {
       const uint32_t lb = tmem + ((uint32_t)(warp * 32) << 16);
       // row r of the tile is finished by rank r >> lper, as its row r & (per - 1).  Rolled: the code runs once
-      // per block, so what counts is the instructions fetched (unrolled eightfold it took 20.5 us, not 9, for
-      // 333 x 1536 x 576)
+      // per block, so what counts is the instructions fetched (unrolled eightfold 333 x 1536 x 576 took 19.1
+      // us, not 7.8, with 128 rows in two)
       const uint32_t mine = smem_u32(smem + C::OFF_X) + (uint32_t)(((rank << lper) * BP + warp * 32 + lane) * 4);
 #pragma unroll 1
       for (int c = 0; c < BT; c += 16) {

@@ -6,11 +6,12 @@
 For every linear group of a decoder layer (q/k/v fused, o, gate/up fused,
 down) it times the forward call (all its kernels), the backward call, the dX
 GEMM alone (no adapter), the causal attention of one layer (forward; backward
-counted as 2.5x the forward FLOPs), and the lm_head GEMMs,
+counted as 2.5x the forward FLOPs), the lm_head GEMMs, and the dense linear at
+the up projection's shape,
 with CUDA events around each launch and a 256 MB L2 flush between launches;
 prints one JSON line per kernel (median ms, TFLOP/s, fraction of the
 measured bf16 peak).  With --hbm it times the memory-bound kernels instead
-(RMSNorm, RoPE, SwiGLU, cross entropy, AdamW, NF4 quantise / dequantise, the
+(RMSNorm, LayerNorm, the 8-bit checkpoint's norm passes, RoPE, SwiGLU, cross entropy, AdamW, NF4 quantise / dequantise, the
 double-quantised absmax expansion, the embedding gather) at the same layer
 sizes and reports their algorithmic bytes (each input read once, each output
 written once) per second against the measured HBM bandwidth.  Inputs are
@@ -85,6 +86,20 @@ def hbm_kernels(sh, M, iters, only=None):
     run("rmsnorm_bwd", 8 * M * d + 4 * M + 2 * d, lambda: L.lsq_rmsnorm_bwd(dy, x, g, rstd, res, dres, M, d))
     Bt = M // 512 if M % 512 == 0 else 1
     Sq = M // Bt
+    db, dg, mean = torch.empty(d, **f32), torch.empty(d, **f32), torch.zeros(M, **f32)
+    run("layernorm_fwd", 4 * M * d + 8 * M + 4 * d, lambda: L.lsq_layernorm_fwd(x, g, g, y, mean, rstd, M, d, sh.eps))
+    wsn = torch.empty(L.lsq_layernorm_bwd_workspace_size(M, d), dtype=torch.uint8, device="cuda")
+    run("layernorm_bwd", 8 * M * d + 8 * M + 10 * d,
+        lambda: L.lsq_layernorm_bwd(dy, x, g, mean, rstd, res, dres, dg, db, 0, M, d, wsn))
+    ck = torch.empty(L.lsq_ckpt8_size(M, d), dtype=torch.uint8, device="cuda")
+    cb = M * d + 2 * M * ((d + 63) // 64)
+    run("rmsnorm_fwd_pack8", 4 * M * d + cb + 4 * M + 2 * d,
+        lambda: L.lsq_rmsnorm_fwd_pack8(x, g, y, rstd, ck, M, d, sh.eps))
+    run("rmsnorm_fwd_unpack8", 4 * M * d + cb + 4 * M + 2 * d,
+        lambda: L.lsq_rmsnorm_fwd_unpack8(ck, g, dres, y, rstd, M, d, sh.eps))
+    run("rmsnorm_bwd_unpack8", 6 * M * d + cb + 4 * M + 2 * d,
+        lambda: L.lsq_rmsnorm_bwd_unpack8(dy, ck, g, rstd, res, dres, M, d))
+    del db, dg, mean, wsn, ck
     run("rope_q", 4 * M * d, lambda: L.lsq_rope(x, Bt, Sq, sh.n_q, sh.hd, sh.theta, 0))
     del x, y, dy, res, dres
     n = M * f
@@ -231,6 +246,17 @@ def main():
     run("lm_head_fwd", 2.0 * M * sh.vocab * sh.d, lambda: L.lsq_dense_gemm(hn, E, logits, M, sh.vocab, sh.d, 0, 1))
     dl = torch.randn(M, sh.vocab, **bf)
     run("lm_head_dx", 2.0 * M * sh.vocab * sh.d, lambda: L.lsq_dense_gemm(dl, E, hn, M, sh.d, sh.vocab, 1, 0))
+    del E, logits, dl
+    # the dense linear at the stack's up projection, tanh-GELU and bias, the pre-activation kept; its backward
+    wu = torch.randn(sh.f, sh.d, **bf) * 0.02
+    bu, z, m = torch.randn(sh.f, **bf), torch.empty(M, sh.f, **bf), torch.empty(M, sh.f, **bf)
+    dxu, dwu = torch.empty(M, sh.d, **bf), torch.empty(sh.f, sh.d, **bf)
+    dbu = torch.empty(sh.f, dtype=torch.float32, device="cuda")
+    wsl = torch.empty(L.lsq_linear_bwd_workspace_size(M, sh.f, sh.d, L.ACT_GELU_TANH), dtype=torch.uint8, device="cuda")
+    fl = 2.0 * M * sh.f * sh.d
+    run("linear_fwd", fl, lambda: L.lsq_linear_fwd(hn, wu, bu, L.ACT_GELU_TANH, None, z, m, M, sh.f, sh.d))
+    run("linear_bwd", 2 * fl, lambda: L.lsq_linear_bwd(m, hn, wu, z, L.ACT_GELU_TANH, dxu, dwu, 0, dbu, 0, M, sh.f,
+                                                       sh.d, wsl))
     return results
 
 

@@ -472,7 +472,7 @@ lsq_status lsq_lora_refresh_bf16(const float* p, void* p_bf16, int64_t n, lsq_cu
  * ---------------------------------------------------------------------- */
 /* LayerNorm: y = (x - mean) rstd g + b per row, mean and variance over d,
  * rstd = 1 / sqrt(var + eps) (variance of the centred values, no cancellation).
- *  x, y     bf16 [rows, d];  g, b bf16 [d] (b may be NULL: no bias)
+ *  x, y     bf16 [rows, d], y may be x;  g, b bf16 [d] (b may be NULL: no bias)
  *  mean, rstd  fp32 [rows], kept for the backward (each may be NULL)
  * d <= 16384, else EUNSUPPORTED. */
 lsq_status lsq_layernorm_fwd(const void* x, const void* g, const void* b, void* y, float* mean, float* rstd,
@@ -480,7 +480,7 @@ lsq_status lsq_layernorm_fwd(const void* x, const void* g, const void* b, void* 
 /* Its backward.  With xh = (x - mean) rstd and a = dy g:
  *   dres_out = dres_in + rstd (a - mean(a) - xh mean(a xh))
  *   dg (+)= sum over rows of dy xh;   db (+)= sum over rows of dy
- *  dres_in  bf16 [rows, d], NULL (treated as 0), may alias dres_out
+ *  dres_in  bf16 [rows, d], NULL (treated as 0); dres_out may be dres_in, dy or x
  *  dg, db   fp32 [d], each may be NULL (frozen)
  *  accumulate  0: overwrite dg / db, 1: add into them
  *  workspace   lsq_layernorm_bwd_workspace_size() bytes, 256-byte aligned, for
@@ -509,7 +509,8 @@ lsq_status lsq_ckpt8_unpack(const void* ckpt, void* x, int64_t rows, int64_t d, 
  *  fwd_unpack8: restores x (bf16, for the residual) and normalises the restored
  *               rows: y and rstd are lsq_rmsnorm_fwd's for them (rstd may be NULL)
  *  bwd_unpack8: lsq_rmsnorm_bwd with the restored rows read from the checkpoint
- * dres_in may be NULL (treated as 0) or alias dres_out. */
+ * dres_in may be NULL (treated as 0); dres_out may be dres_in or dy, and
+ * fwd_pack8's y may be x. */
 lsq_status lsq_rmsnorm_fwd_pack8(const void* x, const void* g, void* y, float* rstd, void* ckpt, int64_t rows,
                                  int64_t d, float eps, lsq_cuda_stream stream);
 lsq_status lsq_rmsnorm_fwd_unpack8(const void* ckpt, const void* g, void* x, void* y, float* rstd, int64_t rows,
@@ -522,9 +523,8 @@ lsq_status lsq_rmsnorm_bwd_unpack8(const void* dy, const void* ckpt, const void*
  * epilogue (fp32, one rounding):
  *   z = x W^T + bias,   y = residual + act(z)
  *  x bf16 [M, K];  w bf16 [N, K];  bias bf16 [N] or NULL
- *  residual  bf16 [M, N] or NULL; may alias y
+ *  residual  bf16 [M, N] or NULL; may be y
  *  z         bf16 [M, N] or NULL: the pre-activation, kept for the backward
- *            (must not alias y or residual)
  *  act       an lsq_act */
 typedef enum lsq_act {
   LSQ_ACT_NONE = 0,

@@ -31,6 +31,12 @@ lsq_status encode_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ba
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// whether [a, a + na) and [b, b + nb) share a byte (no: either is NULL)
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 int num_sms();
 
 // Launch with programmatic stream serialization (and a cluster size, where above 1): the kernel may be set up

@@ -21,6 +21,7 @@
 // 333 x 1536 x 576 6.0; 1 x 4096 x 4096 7.0 (8.7 a call with the weight from HBM).
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "host_common.h"
@@ -818,7 +819,12 @@ extern "C" lsq_status lsq_linear_fwd(const void* x, const void* w, const void* b
   lsq_status st = lin::check_shape(who, M, N, K, act);
   if (st != LSQ_OK) return st;
   if (!nrm::aligned16(x, w, bias, residual, z, y)) return fail(LSQ_EINVAL, "%s: alignment", who);
-  if (z && (z == y || z == residual)) return fail(LSQ_EINVAL, "%s: z must not alias y or residual", who);
+  const size_t mn = (size_t)M * N * 2, mk = (size_t)M * K * 2, nk = (size_t)N * K * 2, n1 = (size_t)N * 2;
+  for (const void* o : {(const void*)y, (const void*)z})
+    if (overlap(o, mn, x, mk) || overlap(o, mn, w, nk) || overlap(o, mn, bias, n1))
+      return fail(LSQ_EINVAL, "%s: an output overlaps x, w or bias", who);
+  if (overlap(z, mn, y, mn) || overlap(z, mn, residual, mn) || nrm::shifted(residual, y, mn))
+    return fail(LSQ_EINVAL, "%s: z, y and residual overlap (residual may be y itself)", who);
   if ((st = check_device()) != LSQ_OK) return st;
   lin::Epi e{};
   e.bias = static_cast<const __nv_bfloat16*>(bias);
@@ -851,7 +857,23 @@ extern "C" lsq_status lsq_linear_bwd(const void* dy, const void* x, const void* 
   if (pass && (!workspace || !aligned(workspace, 256) ||
                workspace_bytes < lsq_linear_bwd_workspace_size(M, N, K, act)))
     return fail(LSQ_EINVAL, "%s: workspace missing, misaligned or too small", who);
+  struct Range {
+    const void* p;
+    size_t n;
+  };
+  const size_t mn = (size_t)M * N * 2, mk = (size_t)M * K * 2, nk = (size_t)N * K * 2;
+  const Range in[] = {{dy, mn}, {x, dw ? mk : 0}, {w, dx ? nk : 0}, {act != LSQ_ACT_NONE ? z : nullptr, mn}};
+  const Range out[] = {{dx, mk}, {dw, dw_f32 ? 2 * nk : nk}, {dbias, (size_t)N * 4},
+                       {pass ? workspace : nullptr, lsq_linear_bwd_workspace_size(M, N, K, act)}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Range& r : in)
+      if (r.n && overlap(out[i].p, out[i].n, r.p, r.n)) return fail(LSQ_EINVAL, "%s: an output overlaps an input", who);
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return fail(LSQ_EINVAL, "%s: outputs overlap", who);
+  }
   if ((st = check_device()) != LSQ_OK) return st;
+  if (pass && workspace_bytes < lsq_linear_bwd_workspace_size(M, N, K, act))  // now that the device's SMs are known
+    return fail(LSQ_EINVAL, "%s: workspace too small for this device", who);
   cudaStream_t s = (cudaStream_t)stream;
   const void* dz = dy;
   if (pass) {

@@ -716,6 +716,10 @@ template <typename... P>
 static bool aligned16(P... p) {
   return (... && aligned(p, 16));
 }
+// an output over its input's bytes at another place: a row would be written before another reads it
+static bool shifted(const void* in, const void* out, size_t bytes) {
+  return in != out && overlap(in, bytes, out, bytes);
+}
 
 }  // namespace nrm
 }  // namespace lsq
@@ -729,6 +733,7 @@ extern "C" lsq_status lsq_layernorm_fwd(const void* x, const void* g, const void
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
   if (!nrm::aligned16(x, g, b, y)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  if (nrm::shifted(x, y, (size_t)rows * d * 2)) return fail(LSQ_EINVAL, "%s: y overlaps x", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Fwd p{};
   p.x = (const uint4*)x;
@@ -756,10 +761,15 @@ extern "C" lsq_status lsq_layernorm_bwd(const void* dy, const void* x, const voi
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
   if (!nrm::aligned16(dy, x, g, dres_in, dres_out, dg, db)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  const size_t xb = (size_t)rows * d * 2;
+  if (nrm::shifted(dy, dres_out, xb) || nrm::shifted(x, dres_out, xb) || nrm::shifted(dres_in, dres_out, xb))
+    return fail(LSQ_EINVAL, "%s: dres_out overlaps an input", who);
   const bool grads = dg || db;
   if (grads && (!workspace || !aligned(workspace, 256) || workspace_bytes < lsq_layernorm_bwd_workspace_size(rows, d)))
     return fail(LSQ_EINVAL, "%s: workspace missing, misaligned or too small", who);
   if ((st = check_device()) != LSQ_OK) return st;
+  if (grads && workspace_bytes < lsq_layernorm_bwd_workspace_size(rows, d))  // now that the device's SMs are known
+    return fail(LSQ_EINVAL, "%s: workspace too small for this device", who);
   nrm::Bwd p{};
   p.dy = (const uint4*)dy;
   p.x = (const uint4*)x;
@@ -800,6 +810,8 @@ extern "C" lsq_status lsq_ckpt8_pack(const void* x, void* ckpt, int64_t rows, in
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
   if (!nrm::aligned16(x, ckpt)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  if (overlap(x, (size_t)rows * d * 2, ckpt, lsq_ckpt8_size(rows, d)))
+    return fail(LSQ_EINVAL, "%s: x overlaps the checkpoint", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Fwd p{};
   p.x = (const uint4*)x;
@@ -813,6 +825,8 @@ extern "C" lsq_status lsq_ckpt8_unpack(const void* ckpt, void* x, int64_t rows, 
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
   if (!nrm::aligned16(x, ckpt)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  if (overlap(x, (size_t)rows * d * 2, ckpt, lsq_ckpt8_size(rows, d)))
+    return fail(LSQ_EINVAL, "%s: x overlaps the checkpoint", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Fwd p{};
   p.xo = (uint4*)x;
@@ -827,6 +841,9 @@ extern "C" lsq_status lsq_rmsnorm_fwd_pack8(const void* x, const void* g, void* 
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
   if (!nrm::aligned16(x, g, y, ckpt)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  const size_t xb = (size_t)rows * d * 2, cb = lsq_ckpt8_size(rows, d);
+  if (nrm::shifted(x, y, xb) || overlap(x, xb, ckpt, cb) || overlap(y, xb, ckpt, cb))
+    return fail(LSQ_EINVAL, "%s: overlapping arguments", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Fwd p{};
   p.x = (const uint4*)x;
@@ -845,6 +862,9 @@ extern "C" lsq_status lsq_rmsnorm_fwd_unpack8(const void* ckpt, const void* g, v
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
   if (!nrm::aligned16(x, g, y, ckpt)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  const size_t xb = (size_t)rows * d * 2, cb = lsq_ckpt8_size(rows, d);
+  if (overlap(x, xb, y, xb) || overlap(x, xb, ckpt, cb) || overlap(y, xb, ckpt, cb))
+    return fail(LSQ_EINVAL, "%s: overlapping arguments", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Fwd p{};
   p.in = nrm::ckpt_of(ckpt, rows, d);
@@ -865,6 +885,10 @@ extern "C" lsq_status lsq_rmsnorm_bwd_unpack8(const void* dy, const void* ckpt, 
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
   if (!nrm::aligned16(dy, ckpt, g, dres_in, dres_out)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  const size_t xb = (size_t)rows * d * 2;
+  if (nrm::shifted(dy, dres_out, xb) || nrm::shifted(dres_in, dres_out, xb) ||
+      overlap(dres_out, xb, ckpt, lsq_ckpt8_size(rows, d)))
+    return fail(LSQ_EINVAL, "%s: dres_out overlaps an input", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Bwd p{};
   p.dy = (const uint4*)dy;

@@ -5,7 +5,7 @@ import torch
 
 from nf4_layer_streamed_blockwise_b200 import lib as L
 
-P = 1 << 20          # a 256-byte aligned address
+P = 1 << 20          # a 256-byte aligned address; the arguments lie 1 MB apart
 S = 0                # the default stream's handle
 EINVAL, EUNSUPPORTED = 1, 6
 
@@ -16,19 +16,32 @@ def _refused(status, fn, *args, **kw):
     assert e.value.status == status, e.value
 
 
+def _at(n):
+    return [P * (k + 1) for k in range(n)]
+
+
+# call, arguments, the ones that must be given, the ones that must be aligned, where rows and d stand, pairs of
+# which the second is written while the first is read (not even the same place where marked True)
 CASES = {
-    "ln_fwd": (L.lsq_layernorm_fwd, [P, P, P, P, P, P, 4, 64, 1e-5], (0, 1, 3), (0, 1, 2, 3), 6),
-    "pack": (L.lsq_ckpt8_pack, [P, P, 4, 64], (0, 1), (0, 1), 2),
-    "unpack": (L.lsq_ckpt8_unpack, [P, P, 4, 64], (0, 1), (0, 1), 2),
-    "fwd_pack8": (L.lsq_rmsnorm_fwd_pack8, [P, P, P, P, P, 4, 64, 1e-5], (0, 1, 2, 4), (0, 1, 2, 4), 5),
-    "fwd_unpack8": (L.lsq_rmsnorm_fwd_unpack8, [P, P, P, P, P, 4, 64, 1e-5], (0, 1, 2, 3), (0, 1, 2, 3), 5),
-    "bwd_unpack8": (L.lsq_rmsnorm_bwd_unpack8, [P, P, P, P, P, P, 4, 64], (0, 1, 2, 3, 5), (0, 1, 2, 4, 5), 6),
+    "ln_fwd": (L.lsq_layernorm_fwd, [*_at(6), 4, 64, 1e-5], (0, 1, 3), (0, 1, 2, 3), 6, [(0, 3, False)]),
+    "pack": (L.lsq_ckpt8_pack, [*_at(2), 4, 64], (0, 1), (0, 1), 2, [(0, 1, True)]),
+    "unpack": (L.lsq_ckpt8_unpack, [*_at(2), 4, 64], (0, 1), (0, 1), 2, [(0, 1, True)]),
+    "fwd_pack8": (L.lsq_rmsnorm_fwd_pack8, [*_at(5), 4, 64, 1e-5], (0, 1, 2, 4), (0, 1, 2, 4), 5,
+                  [(0, 2, False), (0, 4, True), (2, 4, True)]),
+    "fwd_unpack8": (L.lsq_rmsnorm_fwd_unpack8, [*_at(5), 4, 64, 1e-5], (0, 1, 2, 3), (0, 1, 2, 3), 5,
+                    [(0, 2, True), (0, 3, True), (2, 3, True)]),
+    "bwd_unpack8": (L.lsq_rmsnorm_bwd_unpack8, [*_at(6), 4, 64], (0, 1, 2, 3, 5), (0, 1, 2, 4, 5), 6,
+                    [(0, 5, False), (4, 5, False), (1, 5, True)]),
 }
 
 
 @pytest.mark.parametrize("name", sorted(CASES))
 def test_row_passes_refuse(name):
-    fn, args, required, aligned, rows_at = CASES[name]
+    fn, args, required, aligned, rows_at, apart = CASES[name]
+    for a, b, never in apart:
+        _refused(EINVAL, fn, *[args[a] + 128 if k == b else v for k, v in enumerate(args)])
+        if never:
+            _refused(EINVAL, fn, *[args[a] if k == b else v for k, v in enumerate(args)])
     for i in required:
         _refused(EINVAL, fn, *[None if k == i else a for k, a in enumerate(args)])
     for i in aligned:
@@ -42,8 +55,8 @@ def test_layernorm_backward_refuses():
     ws = torch.empty(0, dtype=torch.uint8)
 
     def call(status, **kw):
-        a = dict(dy=P, x=P, g=P, mean=P, rstd=P, dres_in=P, dres_out=P, dg=P, db=P, accumulate=0, rows=4, d=64,
-                 workspace=None)
+        a = dict(zip(("dy", "x", "g", "mean", "rstd", "dres_in", "dres_out", "dg", "db"), _at(9)), accumulate=0,
+                 rows=4, d=64, workspace=None)
         a.update(kw)
         _refused(status, L.lsq_layernorm_bwd, *a.values())
     for k in ("dy", "x", "g", "mean", "rstd", "dres_out"):
@@ -51,6 +64,8 @@ def test_layernorm_backward_refuses():
     for k in ("dy", "x", "g", "dres_in", "dres_out", "dg", "db"):
         call(EINVAL, **{k: P + 8})
     call(EINVAL)                                 # gradients wanted, no workspace
+    for k in (1, 2, 6):                          # dres_out 128 bytes into dy, x, dres_in
+        call(EINVAL, dg=None, db=None, dres_out=P * k + 128)
     call(EINVAL, rows=0)
     call(EINVAL, d=12)
     call(EUNSUPPORTED, d=16392)
@@ -59,24 +74,29 @@ def test_layernorm_backward_refuses():
 
 def test_linear_forward_refuses():
     def call(status, **kw):
-        a = dict(x=P, w=P, bias=P, act=0, residual=P, z=2 * P, y=P, M=4, N=64, K=64)
+        a = dict(x=P, w=2 * P, bias=3 * P, act=0, residual=4 * P, z=5 * P, y=6 * P, M=4, N=64, K=64)
         a.update(kw)
         _refused(status, L.lsq_linear_fwd, *a.values())
     for k in ("x", "w", "y"):
         call(EINVAL, **{k: None})
     for k in ("x", "w", "bias", "residual", "z", "y"):
-        call(EINVAL, **{k: 4 * P + 8})
+        call(EINVAL, **{k: 9 * P + 8})
     for k, v in (("M", 0), ("M", (1 << 30) + 1), ("N", 0), ("N", 60), ("K", 4), ("K", 0), ("K", -8), ("act", -1),
                  ("act", 5)):
         call(EINVAL, **{k: v})
-    call(EINVAL, z=P)                            # z on top of y
-    call(EINVAL, y=3 * P, z=P)                   # z on top of the residual
+    for out in ("y", "z"):                       # an output on x, w, bias, or a few bytes into them
+        for k in (1, 2, 3):
+            call(EINVAL, **{out: k * P})
+            call(EINVAL, **{out: k * P + 64})
+    call(EINVAL, z=6 * P)                        # z on y, z on the residual, y a few rows into the residual
+    call(EINVAL, z=4 * P + 128)
+    call(EINVAL, y=4 * P + 128)
 
 
 def test_linear_backward_refuses():
     def call(status, **kw):
-        a = dict(dy=P, x=P, w=P, z=P, act=2, dx=P, dw=P, dw_f32=1, dbias=P, accumulate=0, M=4, N=64, K=64,
-                 workspace=None)
+        a = dict(dy=P, x=2 * P, w=3 * P, z=4 * P, act=2, dx=5 * P, dw=6 * P, dw_f32=1, dbias=7 * P, accumulate=0,
+                 M=4, N=64, K=64, workspace=None)
         a.update(kw)
         _refused(status, L.lsq_linear_bwd, *a.values())
     call(EINVAL, dy=None)
@@ -90,7 +110,11 @@ def test_linear_backward_refuses():
     call(EINVAL, act=9)
     call(EINVAL, N=20)
     for k in ("dy", "x", "w", "z", "dx", "dw", "dbias"):
-        call(EINVAL, **{k: P + 4})
+        call(EINVAL, **{k: 9 * P + 4})
+    for k in ("dx", "dw"):                       # no activation, no dbias: no workspace, so these reach the check
+        for at in (1, 2, 3):
+            call(EINVAL, act=0, dbias=None, **{k: at * P + 128})
+    call(EINVAL, act=0, dbias=None, dx=6 * P)
 
 
 def test_tensor_arguments_are_checked():

@@ -16,6 +16,9 @@ ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
 SHAPES = [(1, 8, 8), (1, 4096, 4096), (2, 576, 1536), (16, 136, 72), (17, 1536, 576), (33, 640, 2048), (64, 128, 64),
           (65, 264, 520), (127, 1000, 136), (128, 128, 128), (129, 136, 1032), (333, 1536, 576), (300, 64, 8),
           (200, 2304, 8200), (1000, 1160, 328), (2100, 2048, 200), (4000, 16, 72)]
+# with the shapes above, every tile and split of both forms, in the forward and in each gradient (148 SMs)
+TILES = [(2177, 2136, 8), (17, 920, 2400), (1341, 4792, 16), (34, 3944, 1008), (2680, 1032, 1968), (795, 8, 672),
+         (522, 8, 3936), (1051, 8, 2832), (2643, 8, 2928), (335, 2392, 784), (97, 1456, 4768), (265, 2480, 4792)]
 
 
 def _inputs(M, N, K, seed=0):
@@ -36,7 +39,7 @@ def _d(t):
     return None if t is None else t.double()
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("M,N,K", SHAPES + TILES)
 def test_forward(lsq, M, N, K):
     t = _inputs(M, N, K)
     for i, (bias, res, keep) in enumerate([(True, True, True), (False, False, False), (True, False, True),
@@ -63,7 +66,7 @@ def test_forward_in_place_residual_and_repeat(lsq, kind):
     assert torch.equal(h, y)
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("M,N,K", SHAPES + TILES)
 def test_backward(lsq, M, N, K):
     t = _inputs(M, N, K, 2)
     for i in range(2):
@@ -102,6 +105,20 @@ def test_backward_parts_and_accumulation(lsq, kind):
     dwb = torch.empty(N, K, dtype=BF, device="cuda")
     lsq.lsq_linear_bwd(t["dy"], t["x"], None, z, act, None, dwb, 0, None, 0, M, N, K, none_ws)
     assert torch.equal(dwb, dw.to(BF))     # the same sums, rounded once
+
+
+@pytest.mark.parametrize("M,N,K", [(70, 2048, 4096), (2177, 2136, 264), (700, 72, 136)])
+def test_fp32_weight_gradient_accumulates_in_either_form(lsq, M, N, K):
+    """Two accumulating calls on top of a start: one fp32 addition an element and call, in the calls' order."""
+    t, u = _inputs(M, N, K, 6), _inputs(M, N, K, 7)
+    one, two = (torch.empty(N, K, dtype=F32, device="cuda") for _ in range(2))
+    lsq.lsq_linear_bwd(t["dy"], t["x"], None, None, 0, None, one, 1, None, 0, M, N, K, None)
+    lsq.lsq_linear_bwd(u["dy"], u["x"], None, None, 0, None, two, 1, None, 0, M, N, K, None)
+    start = torch.randn(N, K, generator=torch.Generator().manual_seed(1)).cuda()
+    acc = start.clone()
+    for v in (t, u):
+        lsq.lsq_linear_bwd(v["dy"], v["x"], None, None, 0, None, acc, 1, None, 1, M, N, K, None)
+    assert torch.equal(acc, (start + one) + two)
 
 
 @pytest.mark.parametrize("kind", ACTS)

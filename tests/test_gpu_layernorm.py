@@ -146,3 +146,26 @@ def test_rows_behind_the_last_are_left_alone_and_runs_repeat(lsq):
         runs.append((y, out, dg, db))
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,d", [(700, 5120), (77, 1160), (1200, 512), (3, 16384)])
+def test_in_place(lsq, rows, d):
+    """y over x, and the gradient over dy or x, give what separate outputs give."""
+    t = _inputs(rows, d, seed=8)
+    mean, rstd = _stats(t["x"], 1e-5)
+    y = torch.empty_like(t["x"])
+    lsq.lsq_layernorm_fwd(t["x"], t["g"], t["b"], y, None, None, rows, d, 1e-5)
+    x = t["x"].clone()
+    lsq.lsq_layernorm_fwd(x, t["g"], t["b"], x, None, None, rows, d, 1e-5)
+    assert torch.equal(x, y)
+    ws = torch.empty(lsq.lsq_layernorm_bwd_workspace_size(rows, d), dtype=torch.uint8, device="cuda")
+
+    def bwd(dy, x, out):
+        dg, db = (torch.empty(d, dtype=F32, device="cuda") for _ in range(2))
+        lsq.lsq_layernorm_bwd(dy, x, t["g"], mean, rstd, t["res"], out, dg, db, 0, rows, d, ws)
+        return out, dg, db
+    want = bwd(t["dy"], t["x"], torch.empty_like(y))
+    a = t["dy"].clone()
+    b = t["x"].clone()
+    for got in (bwd(a, t["x"], a), bwd(t["dy"], b, b)):
+        assert all(torch.equal(p, q) for p, q in zip(got, want))

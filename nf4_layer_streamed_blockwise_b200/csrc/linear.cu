@@ -11,14 +11,14 @@
 //   dx       p = k, q = m, c = n:  P = W  MN-major,  Q = dz K-major
 //   dW       p = k, q = n, c = m:  P = x  MN-major,  Q = dz MN-major
 //
-// Two forms share them: one tile per cluster with the contraction split (few
+// Two forms share them (one row's forward has a third): one tile per cluster with the contraction split (few
 // tiles: bound by what L2 feeds an SM, and below that by start and exchange)
 // and a persistent CTA-pair form (many tiles: bound by the tensor cores, in a
 // long run by the power cap); plan_product picks by a measured cost model.
 // Measured on B200 (graph replays): 2048 x 14336 x 4096 forward 153-156 us with
 // any activation (1.55 PFLOP/s; 138 us and 86% of the tensor pipe in isolation
 // at full clock), 188 with bias, residual and z kept, dx 165, dW 166;
-// 333 x 1536 x 576 6.0; 1 x 4096 x 4096 7.0 (8.7 a call with the weight from HBM).
+// 333 x 1536 x 576 6.0; 1 x 4096 x 4096 8.0 with the weight from HBM.
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
@@ -630,6 +630,59 @@ static lsq_status launch_pair(const GMaps& maps, const Params& p, int64_t tiles,
                         stream, maps, p);
 }
 
+// ---------------------------------------------------------------- forward of one row
+// A generated token: the weight is read once and HBM decides, so no tensor core and no tile: a block takes
+// eight output columns, its warps share the contraction (warp w the 256-wide steps w, w + 8, ...), a lane
+// multiplies 16-byte words of the eight weight rows with the row's words of x in f32x2, and the warps' sums
+// join in shared memory in warp order.  Eight 16-byte loads a lane and step are in flight.  Weights from HBM,
+// graph replays, against the tiles above: 4096 x 4096 8.0 us (8.9), 14336 x 4096 21.7 (22.6), 576 x 1536 2.4
+// (3.8); the same kernel with two rows loses from 1 M weights on (13.5 us for 9.0: its products take over).
+struct OneRow {
+  const uint4 *x, *w;
+  int N, k8;  // output columns, words of a row
+  Epi e;
+};
+__global__ void __launch_bounds__(256) linear_row_kernel(const __grid_constant__ OneRow p) {
+  __shared__ float part[8][8];
+  grid_release();
+  grid_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = blockIdx.x * 8;
+  const uint4* w = p.w + (int64_t)col * p.k8;
+  uint64_t acc[8];
+#pragma unroll
+  for (int f = 0; f < 8; ++f) acc[f] = 0ull;
+  for (int c = warp * 32 + lane; c < p.k8; c += 256) {
+    uint4 wv[8];
+#pragma unroll
+    for (int f = 0; f < 8; ++f) wv[f] = w[(int64_t)f * p.k8 + c];
+    uint64_t xv[4];
+    nrm::unpack_pairs(p.x[c], xv);
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+      uint64_t u[4];
+      nrm::unpack_pairs(wv[f], u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[f] = fma2(xv[j], u[j], acc[f]);
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < 8; ++f) {
+    const float v = nrm::warp_sum(nrm::pair_sum(acc[f]));
+    if (lane == 0) part[warp][f] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  float v[8];
+#pragma unroll
+  for (int f = 0; f < 8; ++f) {
+    v[f] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[f] += part[k][f];
+  }
+  finish8(v, p.e, col, col);
+}
+
 // K-major operand [rows, C] with box {64, brows}; MN-major operand [C, rows] with box {64, 64}
 static lsq_status map_operand(CUtensorMap* m, const void* base, int mn, int64_t rows, int64_t contraction, int brows) {
   return mn ? encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, contraction, rows * 2, 64, BK,
@@ -832,6 +885,11 @@ extern "C" lsq_status lsq_linear_fwd(const void* x, const void* w, const void* b
   e.z = static_cast<__nv_bfloat16*>(z);
   e.out = y;
   e.act = act;
+  if (M == 1) {
+    const lin::OneRow p{(const uint4*)x, (const uint4*)w, (int)N, (int)(K / 8), e};
+    return launch_chained("linear_row_kernel", lin::linear_row_kernel, dim3((unsigned)(N / 8)), 256, 0, 1,
+                          (cudaStream_t)stream, p);
+  }
   return lin::product<0, 0>(w, x, N, M, K, e, (cudaStream_t)stream);
 }
 

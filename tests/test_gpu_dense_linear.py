@@ -13,7 +13,7 @@ ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
 
 # (M, N, K): one row, every tile width of the split kernel, its contraction splits, ragged edges in each
 # direction, contractions shorter than one block, more tiles than SMs
-SHAPES = [(1, 8, 8), (1, 4096, 4096), (2, 576, 1536), (16, 136, 72), (17, 1536, 576), (33, 640, 2048), (64, 128, 64),
+SHAPES = [(1, 8, 8), (1, 4096, 4096), (1, 72, 2056), (1, 1000, 264), (1, 264, 8200), (2, 576, 1536), (16, 136, 72), (17, 1536, 576), (33, 640, 2048), (64, 128, 64),
           (65, 264, 520), (127, 1000, 136), (128, 128, 128), (129, 136, 1032), (333, 1536, 576), (300, 64, 8),
           (200, 2304, 8200), (1000, 1160, 328), (2100, 2048, 200), (4000, 16, 72)]
 # with the shapes above, every tile and split of both forms, in the forward and in each gradient (148 SMs)

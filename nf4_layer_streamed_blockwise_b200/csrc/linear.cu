@@ -794,21 +794,23 @@ static lsq_status product(const void* pop, const void* qop, int64_t P, int64_t Q
 
 // ---------------------------------------------------------------- dz and db
 // dz = dy act'(z) (bf16: the products' operand type) and, from the fp32 dz, the sums over a strip of rows;
-// a warp covers 256 columns of a row (16 bytes a lane), a block's eight warps take rows in turn, and the
-// strips' sums are added in order by col_sum_kernel.
+// a warp covers 256 columns of a row (16 bytes a lane), a block's eight warps take rows in turn.  Where at most
+// eight strips fill the GPU or the rows are few, a cluster holds a column block's strips (cs) and its first block
+// adds them in order into dbias; else each strip leaves a row of part for col_sum_kernel.
 template <int ACT>
 __global__ void __launch_bounds__(256, 4) dz_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ z,
-                                                 uint4* __restrict__ dz, float* __restrict__ part, int64_t rows, int n8,
-                                                 int64_t strip) {
+                                                    uint4* __restrict__ dz, float* __restrict__ part, int64_t rows, int n8,
+                                                    int64_t strip, int strips, int cs, float* dbias, int accumulate) {
   __shared__ float comb[8][32][9];
+  __shared__ float4 own[64];
   grid_release();
   grid_wait();
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  const int c = blockIdx.x * 32 + l;
-  const int64_t r0 = blockIdx.y * strip, r1 = r0 + strip < rows ? r0 + strip : rows;
+  const int at = (int)blockIdx.x % strips, c = ((int)blockIdx.x / strips) * 32 + l;
+  const int64_t r0 = at * strip, r1 = r0 + strip < rows ? r0 + strip : rows;
   uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
   if (c < n8) {
-#pragma unroll 4
+#pragma unroll (ACT == LSQ_ACT_RELU ? 2 : 4)  // rows in flight: ReLU 29 us with 2, 34 with 4 (2048 x 14336); GELU 40, 38
     for (int64_t r = r0 + w; r < r1; r += 8) {
       uint64_t d[4];
       nrm::unpack_pairs(dy[r * n8 + c], d);
@@ -825,26 +827,57 @@ __global__ void __launch_bounds__(256, 4) dz_kernel(const uint4* __restrict__ dy
   }
   float s[8];
   nrm::split8(acc, s);
-  if (!part) return;
+  if (!dbias) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) comb[w][l][j] = s[j];
   __syncthreads();
-  if (w != 0 || c >= n8) return;
+  if (w == 0) {
 #pragma unroll
-  for (int k = 1; k < 8; ++k)
+    for (int k = 1; k < 8; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] += comb[k][l][j];
-  float4* o = reinterpret_cast<float4*>(part + ((int64_t)blockIdx.y * n8 + c) * 8);
-  o[0] = make_float4(s[0], s[1], s[2], s[3]);
-  o[1] = make_float4(s[4], s[5], s[6], s[7]);
+      for (int j = 0; j < 8; ++j) s[j] += comb[k][l][j];
+    float4* o = cs ? own + l * 2 : reinterpret_cast<float4*>(part + ((int64_t)at * n8 + c) * 8);
+    if (cs || c < n8) {
+      o[0] = make_float4(s[0], s[1], s[2], s[3]);
+      o[1] = make_float4(s[4], s[5], s[6], s[7]);
+    }
+  }
+  if (!cs) return;
+  if (cs > 1) nf4g::cluster_sync_all();
+  else __syncthreads();
+  const int word = (int)threadIdx.x >> 1;  // 64 threads of the cluster's first block, four columns each
+  if (at == 0 && threadIdx.x < 64 && ((int)blockIdx.x / strips) * 32 + word < n8) {
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < cs; ++k) {
+      const float4 v = nf4g::ldn::ld_dsmem_f4(nf4g::cluster_addr(own + threadIdx.x, (uint32_t)k));
+      t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+    }
+    float4* o = reinterpret_cast<float4*>(dbias) + ((int64_t)((int)blockIdx.x / strips) * 64 + threadIdx.x);
+    if (accumulate) {
+      const float4 v = *o;
+      t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+    }
+    *o = t;
+  }
+  if (cs > 1) nf4g::cluster_sync_all();  // the sums stay until the first block has read them
 }
 
-// row strips of dz_kernel: one round of its blocks (four per SM), at least 8 rows each
-static int64_t strips_of(int64_t M, int64_t N) {
-  const int64_t cb = (N + 255) / 256;
-  const int64_t want = std::max<int64_t>(1, 4 * num_sms() / cb);
-  const int64_t rows = std::max<int64_t>(8, (M + want - 1) / want);
-  return (M + rows - 1) / rows;
+// row strips of dz_kernel: one round of its blocks (four per SM), at least 8 rows each; at most eight, joined in a
+// cluster, where they fill that round or leave no more than 4 rows a warp (2048 x 14336, 448 of 592 blocks: 43 us
+// joined, 38 with ten strips and a second kernel)
+struct Strips {
+  int64_t rows;
+  int n, joined;
+};
+static Strips strips_of(int64_t M, int64_t N) {
+  const int64_t cb = (N + 255) / 256, slots = 4 * num_sms();
+  const bool join = 8 * cb >= slots || M <= 256;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(slots / cb, join ? 8 : slots));
+  Strips s;
+  s.rows = std::max<int64_t>(8, (M + want - 1) / want);
+  s.n = (int)((M + s.rows - 1) / s.rows);
+  s.joined = s.n <= 8;
+  return s;
 }
 static size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -896,7 +929,7 @@ extern "C" lsq_status lsq_linear_fwd(const void* x, const void* w, const void* b
 extern "C" size_t lsq_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act) {
   if (M < 1 || N < 8 || K < 8) return 256;
   return (act == LSQ_ACT_NONE ? 0 : lin::round256((size_t)M * (size_t)N * 2)) +
-         lin::round256((size_t)lin::strips_of(M, N) * (size_t)N * sizeof(float));
+         lin::round256((size_t)lin::strips_of(M, N).n * (size_t)N * sizeof(float));
 }
 
 extern "C" lsq_status lsq_linear_bwd(const void* dy, const void* x, const void* w, const void* z, int32_t act, void* dx,
@@ -940,20 +973,21 @@ extern "C" lsq_status lsq_linear_bwd(const void* dy, const void* x, const void* 
       dz = ws;
       ws += lin::round256((size_t)M * (size_t)N * 2);
     }
-    float* part = dbias ? reinterpret_cast<float*>(ws) : nullptr;
-    const int64_t strips = lin::strips_of(M, N), strip = (M + strips - 1) / strips;
-    const int ns = (int)((M + strip - 1) / strip);
-    const dim3 grid((unsigned)((N + 255) / 256), (unsigned)ns);
-    const int n8 = (int)(N / 8);
+    float* part = reinterpret_cast<float*>(ws);
+    const lin::Strips sp = lin::strips_of(M, N);
+    const int64_t blocks = (N + 255) / 256 * sp.n;
+    const int n8 = (int)(N / 8), cs = sp.joined ? sp.n : 0;
     auto k = act == LSQ_ACT_RELU        ? lin::dz_kernel<LSQ_ACT_RELU>
              : act == LSQ_ACT_GELU      ? lin::dz_kernel<LSQ_ACT_GELU>
              : act == LSQ_ACT_GELU_TANH ? lin::dz_kernel<LSQ_ACT_GELU_TANH>
              : act == LSQ_ACT_SILU      ? lin::dz_kernel<LSQ_ACT_SILU>
                                         : lin::dz_kernel<LSQ_ACT_NONE>;
-    st = launch_chained("dz_kernel", k, grid, 256, 0, 1, s, (const uint4*)dy, (const uint4*)z,
-                        act == LSQ_ACT_NONE ? (uint4*)nullptr : (uint4*)const_cast<void*>(dz), part, M, n8, strip);
+    st = launch_chained("dz_kernel", k, dim3((unsigned)blocks), 256, 0, cs > 1 ? (unsigned)cs : 1u, s, (const uint4*)dy,
+                        (const uint4*)z, act == LSQ_ACT_NONE ? (uint4*)nullptr : (uint4*)const_cast<void*>(dz), part, M,
+                        n8, sp.rows, sp.n, cs, dbias, accumulate ? 1 : 0);
     if (st != LSQ_OK) return st;
-    if (dbias && (st = nrm::col_sum(part, ns, N, N, N, dbias, nullptr, accumulate ? 1 : 0, s)) != LSQ_OK) return st;
+    if (dbias && !cs && (st = nrm::col_sum(part, sp.n, N, N, N, dbias, nullptr, accumulate ? 1 : 0, s)) != LSQ_OK)
+      return st;
   }
   if (dx) {
     lin::Epi e{};

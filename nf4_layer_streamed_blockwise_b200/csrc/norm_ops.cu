@@ -352,21 +352,41 @@ __device__ __forceinline__ uint4 ln_bwd_out(const uint64_t (&xh)[4], const uint6
   for (int j = 0; j < 4; ++j) o[j] = fma2(xh[j], nk2, add2(fma2(a[j], rs, o[j]), nk1));
   return pack_pairs(o);
 }
-// this thread's eight column sums of word c, to the block's partial row or (one block) to dg / db
-__device__ __forceinline__ void ln_put_sums(const Bwd& p, int h, int c, const float (&v)[8]) {
-  const bool one = gridDim.x == 1;
+// eight column sums of word c, to row r of the partial sums or (last) to dg / db
+__device__ __forceinline__ void ln_put_sums(const Bwd& p, int r, bool last, int h, int c, const float (&v)[8]) {
   const int d = p.d8 * 8;
-  float* o = one ? (h ? p.db : p.dg) : p.part + ((int64_t)blockIdx.x * 2 + h) * d;
+  float* o = last ? (h ? p.db : p.dg) : p.part + ((int64_t)r * 2 + h) * d;
   if (!o) return;
   float4* o4 = reinterpret_cast<float4*>(o + c * 8);
   float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
-  if (one && p.accumulate) {
+  if (last && p.accumulate) {
     const float4 x = o4[0], y = o4[1];
     lo.x += x.x; lo.y += x.y; lo.z += x.z; lo.w += x.w;
     hi.x += y.x; hi.y += y.y; hi.z += y.z; hi.w += y.w;
   }
   o4[0] = lo;
   o4[1] = hi;
+}
+// Few rows: the blocks are one cluster, each leaves its sums in shared memory (xs: [h][d / 4]), and each finishes
+// its share of the words from all of them, in rank order: no second kernel (a launch costs the host 2.4 us).
+constexpr int MAX_CS = 8;
+__device__ __forceinline__ void ln_join_sums(const Bwd& p, const float4* xs, int cs) {
+  nf4g::cluster_sync_all();
+  const int d8 = p.d8, n = (int)blockDim.x;
+  for (int it = (int)nf4g::cluster_ctarank() * n + (int)threadIdx.x; it < 2 * d8; it += cs * n) {
+    const int h = it >= d8, c = it - h * d8;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    for (int k = 0; k < cs; ++k) {
+      const uint32_t a = nf4g::cluster_addr(xs + it * 2, (uint32_t)k);
+      const float4 lo = nf4g::ldn::ld_dsmem_f4(a), hi = nf4g::ldn::ld_dsmem_f4(a + 16);
+      v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+      v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+    }
+    ln_put_sums(p, 0, true, h, c, v);
+  }
+  nf4g::cluster_sync_all();  // the sums stay until every block has read its share
 }
 __device__ __forceinline__ void split8(const uint64_t* s, float (&v)[8]) {
 #pragma unroll
@@ -390,9 +410,10 @@ __device__ __forceinline__ void ln_fetch(const Bwd& p, uint8_t* b, uint64_t* bar
 // a row per warp, V words a lane
 constexpr int LNW = 8;
 template <int V, bool GRADS>
-__global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_constant__ Bwd p, int nst, int stage) {
+__global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_constant__ Bwd p, int nst, int stage, int cs) {
   extern __shared__ __align__(128) uint8_t smem[];  // per warp [nst][x | dy | res], then every stage's barrier
   __shared__ float comb[LNW * 32 * 9];
+  __shared__ float4 xs[GRADS ? 2 * V * 64 : 1];  // this block's sums, for ln_join_sums
   const int t = (int)(threadIdx.x & 31), w = (int)(threadIdx.x >> 5);
   uint8_t* ring = smem + (size_t)w * nst * stage;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)LNW * nst * stage) + w * nst;
@@ -464,9 +485,15 @@ __global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_c
         for (int k = 1; k < LNW; ++k)
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] += comb[(k * 32 + t) * 9 + j];
-        ln_put_sums(p, h, c, v);
+        if (cs == 1) {
+          ln_put_sums(p, (int)blockIdx.x, gridDim.x == 1, h, c, v);
+        } else {
+          xs[(h * d8 + c) * 2] = make_float4(v[0], v[1], v[2], v[3]);
+          xs[(h * d8 + c) * 2 + 1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
       }
     }
+    if (cs > 1) ln_join_sums(p, xs, cs);
   }
 }
 
@@ -474,7 +501,7 @@ __global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_c
 // every thread is then done with it.
 template <int V, bool GRADS>
 __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
-    ln_bwd_block_kernel(const __grid_constant__ Bwd p, int nst, int stage) {
+    ln_bwd_block_kernel(const __grid_constant__ Bwd p, int nst, int stage, int cs) {
   extern __shared__ __align__(128) uint8_t ring[];  // [nst][x | dy | res], then the stages' barriers
   __shared__ float2 red[2][16];
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)nst * stage);
@@ -544,16 +571,25 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
     if (++s == nst) s = 0, ph ^= 1;
   }
   if constexpr (GRADS) {
+    float4* xs = reinterpret_cast<float4*>(ring);  // in place of the ring
+    if (cs > 1) __syncthreads();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = t + i * T;
       if (c >= d8) break;
-      float v[8];
-      split8(sg[i], v);
-      ln_put_sums(p, 0, c, v);
-      split8(sb[i], v);
-      ln_put_sums(p, 1, c, v);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[8];
+        split8(h ? sb[i] : sg[i], v);
+        if (cs == 1) {
+          ln_put_sums(p, (int)blockIdx.x, gridDim.x == 1, h, c, v);
+        } else {
+          xs[(h * d8 + c) * 2] = make_float4(v[0], v[1], v[2], v[3]);
+          xs[(h * d8 + c) * 2 + 1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      }
     }
+    if (cs > 1) ln_join_sums(p, xs, cs);
   }
 }
 
@@ -636,11 +672,11 @@ static Geo row_geo(int64_t rows, int d8, Pass pass) {
 // reductions (two blocks of 320 threads: 63 us for 8192 x 5120; one block of two such groups, which halves
 // the partial sums: 72) and share its registers and shared memory (rings of nst stages of `stage` bytes).
 struct BwdGeo {
-  int v, threads, warp, nst, stage;
+  int v, threads, warp, nst, stage, cluster;
   unsigned blocks;
 };
 constexpr int RING_BYTES = 200 * 1024;
-static BwdGeo ln_bwd_geo(int64_t rows, int d8) {
+static BwdGeo ln_bwd_geo(int64_t rows, int d8, bool grads) {
   BwdGeo g{};
   g.stage = (3 * d8 * 16 + 127) / 128 * 128;
   g.warp = d8 <= 96;
@@ -655,7 +691,11 @@ static BwdGeo ln_bwd_geo(int64_t rows, int d8) {
     occ = g.v == 4 ? (g.threads <= 256 ? 2 : 1) : std::max(2, std::min(6, 640 / g.threads));
   }
   g.nst = std::max(2, std::min(8, RING_BYTES / occ / per / g.stage));
-  g.blocks = (unsigned)std::min<int64_t>((rows + per - 1) / per, (int64_t)occ * num_sms());
+  // up to two rows a walker of one cluster: its blocks join their sums themselves (130 x 576 7.8 us in one launch,
+  // 5.7 in two, but the second costs the host 2.4; at 333 x 576 it would be 11.7 for 5.7)
+  const bool few = grads && rows <= 2 * (int64_t)per * MAX_CS;
+  g.blocks = (unsigned)std::min<int64_t>((rows + per - 1) / per, few ? MAX_CS : (int64_t)occ * num_sms());
+  g.cluster = few ? (int)g.blocks : 1;
   return g;
 }
 
@@ -691,12 +731,12 @@ static lsq_status run_ln_bwd(const Bwd& p, const BwdGeo& g, cudaStream_t s) {
     lsq_status st = ring_smem(ln_bwd_warp_kernel<V, GRADS>, configured);
     if (st != LSQ_OK) return st;
     return launch_chained("ln_bwd_warp_kernel", ln_bwd_warp_kernel<V, GRADS>, dim3(g.blocks), (unsigned)g.threads, smem,
-                          1, s, p, g.nst, g.stage);
+                          (unsigned)g.cluster, s, p, g.nst, g.stage, g.cluster);
   } else {
     lsq_status st = ring_smem(ln_bwd_block_kernel<V, GRADS>, configured);
     if (st != LSQ_OK) return st;
     return launch_chained("ln_bwd_block_kernel", ln_bwd_block_kernel<V, GRADS>, dim3(g.blocks), (unsigned)g.threads,
-                          smem, 1, s, p, g.nst, g.stage);
+                          smem, (unsigned)g.cluster, s, p, g.nst, g.stage, g.cluster);
   }
 }
 template <int V, bool WARP>
@@ -748,7 +788,7 @@ extern "C" lsq_status lsq_layernorm_fwd(const void* x, const void* g, const void
 
 extern "C" size_t lsq_layernorm_bwd_workspace_size(int64_t rows, int64_t d) {
   if (rows < 1 || d < 8 || d > nrm::MAX_D) return 256;
-  const nrm::BwdGeo g = nrm::ln_bwd_geo(rows, (int)(d / 8));
+  const nrm::BwdGeo g = nrm::ln_bwd_geo(rows, (int)(d / 8), true);
   return ((size_t)g.blocks * 2 * (size_t)d * sizeof(float) + 255) / 256 * 256;
 }
 
@@ -785,7 +825,7 @@ extern "C" lsq_status lsq_layernorm_bwd(const void* dy, const void* x, const voi
   p.d8 = (int)(d / 8);
   p.accumulate = accumulate ? 1 : 0;
   p.inv_d = 1.0f / (float)d;
-  const nrm::BwdGeo ge = nrm::ln_bwd_geo(rows, p.d8);
+  const nrm::BwdGeo ge = nrm::ln_bwd_geo(rows, p.d8, grads);
   cudaStream_t s = (cudaStream_t)stream;
   if (ge.warp)
     st = ge.v == 1   ? nrm::run_ln_bwd<1, true>(p, grads, ge, s)
@@ -794,7 +834,7 @@ extern "C" lsq_status lsq_layernorm_bwd(const void* dy, const void* x, const voi
   else
     st = ge.v == 2 ? nrm::run_ln_bwd<2, false>(p, grads, ge, s) : nrm::run_ln_bwd<4, false>(p, grads, ge, s);
   if (st != LSQ_OK) return st;
-  if (!grads || ge.blocks == 1) return LSQ_OK;
+  if (!grads || ge.blocks == (unsigned)ge.cluster) return LSQ_OK;
   return nrm::col_sum(p.part, (int)ge.blocks, 2 * d, d, 2 * d, dg, db, p.accumulate, s);
 }
 

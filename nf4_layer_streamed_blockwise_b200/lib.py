@@ -616,8 +616,8 @@ def lsq_layernorm_bwd(dy, x, g, mean, rstd, dres_in, dres_out, dg, db, accumulat
                       stream=None):
     """dres_out = dres_in + dx; dg, db fp32 (None: frozen), overwritten or (accumulate=1) added to."""
     f, dev, n, bf, f32 = "lsq_layernorm_bwd", _dev(), rows * d, torch.bfloat16, torch.float32
-    # the rows of one block (8 of at most 768 columns, else one) need no second kernel
-    two = (dg is not None or db is not None) and rows > (8 if d <= 768 else 1)
+    # few rows (one cluster's) need no second kernel
+    two = (dg is not None or db is not None) and rows > (128 if d <= 768 else 16)
     _call(f, _t(f, "dy", dy, bf, n, dev), _t(f, "x", x, bf, n, dev), _t(f, "g", g, bf, d, dev),
           _t(f, "mean", mean, f32, rows, dev), _t(f, "rstd", rstd, f32, rows, dev),
           _t(f, "dres_in", dres_in, bf, n, dev), _t(f, "dres_out", dres_out, bf, n, dev), _t(f, "dg", dg, f32, d, dev),
@@ -687,7 +687,8 @@ def lsq_linear_bwd(dy, x, w, z, act: int, dx, dw, dw_f32: int, dbias, accumulate
                    workspace, stream=None):
     """dx, dw and dbias (each may be None) of lsq_linear_fwd from dy and the kept pre-activation z."""
     f, dev, mn, bf, f32 = "lsq_linear_bwd", _dev(), M * N, torch.bfloat16, torch.float32
-    launches = (1 if act != ACT_NONE or dbias is not None else 0) + sum(t is not None for t in (dbias, dx, dw))
+    # at least: a tall dz pass adds a kernel for dbias
+    launches = (1 if act != ACT_NONE or dbias is not None else 0) + (dx is not None) + (dw is not None)
     _call(f, _t(f, "dy", dy, bf, mn, dev), _t(f, "x", x, bf, M * K, dev), _t(f, "w", w, bf, N * K, dev),
           _t(f, "z", z, bf, mn, dev), act, _t(f, "dx", dx, bf, M * K, dev),
           _t(f, "dw", dw, f32 if dw_f32 else bf, N * K, dev), dw_f32, _t(f, "dbias", dbias, f32, N, dev), accumulate,

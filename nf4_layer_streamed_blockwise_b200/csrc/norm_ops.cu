@@ -595,38 +595,35 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
 
 // out0[c] (+)= sum over the G rows of part[.][c] for c < n0, out1[c - n0] for the columns from n0 on
 // (either may be null; n0 and ncols even); part has row stride ld.  Warp w of 32 takes rows w, w + 32, ...,
-// eight loads in flight, and the warps' sums are added in order.
+// ten loads in flight (two blocks' rows on 148 SMs are one batch); then warp w adds column pair w's 32 sums.
 __global__ void __launch_bounds__(1024) col_sum_kernel(const float* __restrict__ part, int G, int64_t ld, int64_t n0,
                                                        int64_t ncols, float* out0, float* out1, int accumulate) {
   __shared__ float2 s[32][33];
   grid_release();
   grid_wait();
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  const int64_t c = ((int64_t)blockIdx.x * 32 + l) * 2;
+  const int64_t c0 = (int64_t)blockIdx.x * 64, c = c0 + l * 2;
   float2 v = make_float2(0.0f, 0.0f);
   if (c < ncols)
-    for (int r0 = w; r0 < G; r0 += 256) {
-      float2 u[8];
+    for (int r0 = w; r0 < G; r0 += 320) {
+      float2 u[10];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 10; ++i)
         u[i] = r0 + i * 32 < G ? *reinterpret_cast<const float2*>(part + (r0 + i * 32) * ld + c)
                                : make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 10; ++i) {
         v.x += u[i].x;
         v.y += u[i].y;
       }
     }
   s[w][l] = v;
   __syncthreads();
-  if (w != 0 || c >= ncols) return;
-  float2 tot = make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    tot.x += s[k][l].x;
-    tot.y += s[k][l].y;
-  }
-  float* o = c < n0 ? (out0 ? out0 + c : nullptr) : (out1 ? out1 + (c - n0) : nullptr);
+  const float2 x = s[l][w];
+  float2 tot = make_float2(warp_sum(x.x), warp_sum(x.y));
+  const int64_t cw = c0 + w * 2;
+  if (l != 0 || cw >= ncols) return;
+  float* o = cw < n0 ? (out0 ? out0 + cw : nullptr) : (out1 ? out1 + (cw - n0) : nullptr);
   if (!o) return;
   if (accumulate) {
     tot.x += o[0];

@@ -687,11 +687,15 @@ static BwdGeo ln_bwd_geo(int64_t rows, int d8, bool grads) {
     g.threads = (((d8 + g.v - 1) / g.v) + 31) / 32 * 32;
     occ = g.v == 4 ? (g.threads <= 256 ? 2 : 1) : std::max(2, std::min(6, 640 / g.threads));
   }
-  g.nst = std::max(2, std::min(8, RING_BYTES / occ / per / g.stage));
   // up to two rows a walker of one cluster: its blocks join their sums themselves (130 x 576 7.8 us in one launch,
   // 5.7 in two, but the second costs the host 2.4; at 333 x 576 it would be 11.7 for 5.7)
   const bool few = grads && rows <= 2 * (int64_t)per * MAX_CS;
-  g.blocks = (unsigned)std::min<int64_t>((rows + per - 1) / per, few ? MAX_CS : (int64_t)occ * num_sms());
+  // each block's sums are 8 d bytes to write and to add: whole rounds of blocks with about four rows each pay for
+  // them (1000 x 2048: 9.5 / 8.3 / 9.0 / 10.8 / 12.4 us with 1 to 5 blocks per SM; 10.2 with 250 blocks)
+  if (grads && !few && !g.warp) occ = (int)std::min<int64_t>(occ, (rows + 4 * num_sms() - 1) / (4 * num_sms()));
+  g.nst = std::max(2, std::min(8, RING_BYTES / occ / per / g.stage));
+  const int64_t most = few ? MAX_CS : (int64_t)occ * num_sms();
+  g.blocks = (unsigned)std::min((rows + per - 1) / per, most);
   g.cluster = few ? (int)g.blocks : 1;
   return g;
 }

@@ -11,9 +11,9 @@
 // Measured on B200 in graph replays over three sets of buffers, 8192 x 5120
 // (a copy of the same tensor runs at 6.1 TB/s): LayerNorm forward 31.4 us
 // (5.3 TB/s: its two dependent reductions a row), backward with frozen gain
-// 53.0 (6.3 TB/s), with dg and db 62.2 (the 12 MB of partial sums and their
+// 53.0 (6.3 TB/s), with dg and db 61.3 (the 12 MB of partial sums and their
 // second kernel), norm and checkpoint 35.2 (6.0), restore and norm 34.1 (6.2),
-// backward from the checkpoint 50.8 (5.8).  2048 x 4096: 8.2, 15.6, 21.5, 9.2,
+// backward from the checkpoint 50.8 (5.8).  2048 x 4096: 8.2, 15.6, 21.2, 9.2,
 // 8.5, 11.6 us.  One row of 4096: 2.2 us, launch and latency.
 #include <algorithm>
 
@@ -258,8 +258,8 @@ struct Bwd {
   const float *mean, *rstd;
   const uint4* res;   // dres_in or null; may alias out
   uint4* out;
-  float* part;        // [gridDim.x][2][d]: this block's sums of dy xhat and dy (GRADS)
-  float *dg, *db;     // written here when the grid is one block
+  float* part;        // [gridDim.x][2][d]: the blocks' sums of dy xhat and dy (GRADS)
+  float *dg, *db;     // written here when the grid is one block or one cluster
   int64_t rows;
   int d8, nb, accumulate;
   float inv_d;
@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) rms_bwd_unpa
 // or blocks walk the rows in strides and a thread's columns stay the same, so the sums over rows of dy xh
 // and dy (dg, db) collect in registers and leave once per block; col_sum_kernel adds the blocks in order.
 // The arithmetic runs on pairs (f32x2): scalar, its 30 operations an element took as long as the loads.
+
 // one word of the first pass: xh and a, their row sums, and the column sums of dy xh and dy
 template <bool GRADS>
 __device__ __forceinline__ void ln_bwd_word(uint4 x, uint4 dy, uint4 g, uint64_t nmu, uint64_t rs, uint64_t (&xh)[4],
@@ -666,7 +667,7 @@ static Geo row_geo(int64_t rows, int d8, Pass pass) {
   return g;
 }
 // Backward: a row a warp (eight warps a block) or a row a block; `occ` blocks per SM hide one another's row
-// reductions (two blocks of 320 threads: 63 us for 8192 x 5120; one block of two such groups, which halves
+// reductions (two blocks of 320 threads: 61 us for 8192 x 5120; one block of two such groups, which halves
 // the partial sums: 72) and share its registers and shared memory (rings of nst stages of `stage` bytes).
 struct BwdGeo {
   int v, threads, warp, nst, stage, cluster;

@@ -587,25 +587,31 @@ def _t(fn: str, name: str, t, dtype, n: int, dev: int) -> Optional[int]:
     None and raw addresses pass through."""
     if t is None or t.__class__ is int:
         return t
-    if dtype is None:
-        short = t.numel() * t.element_size() < n
-    else:
-        short = t.dtype is not dtype or t.numel() < n
-    if short or not t.is_contiguous() or t.get_device() != dev:
+    if t.dtype is dtype and t.numel() >= n and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    if dtype is not None or t.numel() * t.element_size() < n or not t.is_contiguous() or t.get_device() != dev:
         _bad(fn, name, t, dtype, n)
     return t.data_ptr()
 
 
-def _dev() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2   # -2: no tensor is on it
+_cur_dev = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _here(stream):
+    """The current device's index (-2, no tensor's, before CUDA is up) and the stream's handle."""
+    if not torch.cuda.is_initialized():
+        return -2, _stream(stream)
+    dev = _cur_dev()
+    return dev, _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def lsq_layernorm_fwd(x, g, b, y, mean, rstd, rows: int, d: int, eps: float, stream=None):
     """y = (x - mean) rstd g + b; b, mean and rstd may be None."""
-    f, dev, n, bf, f32 = "lsq_layernorm_fwd", _dev(), rows * d, torch.bfloat16, torch.float32
+    f, n, bf, f32 = "lsq_layernorm_fwd", rows * d, torch.bfloat16, torch.float32
+    dev, st = _here(stream)
     _call(f, _t(f, "x", x, bf, n, dev), _t(f, "g", g, bf, d, dev), _t(f, "b", b, bf, d, dev),
           _t(f, "y", y, bf, n, dev), _t(f, "mean", mean, f32, rows, dev), _t(f, "rstd", rstd, f32, rows, dev), rows, d,
-          eps, _stream(stream))
+          eps, st)
 
 
 def lsq_layernorm_bwd_workspace_size(rows: int, d: int) -> int:
@@ -615,14 +621,15 @@ def lsq_layernorm_bwd_workspace_size(rows: int, d: int) -> int:
 def lsq_layernorm_bwd(dy, x, g, mean, rstd, dres_in, dres_out, dg, db, accumulate: int, rows: int, d: int, workspace,
                       stream=None):
     """dres_out = dres_in + dx; dg, db fp32 (None: frozen), overwritten or (accumulate=1) added to."""
-    f, dev, n, bf, f32 = "lsq_layernorm_bwd", _dev(), rows * d, torch.bfloat16, torch.float32
+    f, n, bf, f32 = "lsq_layernorm_bwd", rows * d, torch.bfloat16, torch.float32
+    dev, st = _here(stream)
     # few rows (one cluster's) need no second kernel
     two = (dg is not None or db is not None) and rows > (128 if d <= 768 else 16)
     _call(f, _t(f, "dy", dy, bf, n, dev), _t(f, "x", x, bf, n, dev), _t(f, "g", g, bf, d, dev),
           _t(f, "mean", mean, f32, rows, dev), _t(f, "rstd", rstd, f32, rows, dev),
           _t(f, "dres_in", dres_in, bf, n, dev), _t(f, "dres_out", dres_out, bf, n, dev), _t(f, "dg", dg, f32, d, dev),
           _t(f, "db", db, f32, d, dev), accumulate, rows, d, _t(f, "workspace", workspace, None, 0, dev),
-          _nbytes(workspace), _stream(stream), launches=2 if two else 1)
+          _nbytes(workspace), st, launches=2 if two else 1)
 
 
 def lsq_ckpt8_size(rows: int, d: int) -> int:
@@ -636,47 +643,52 @@ def _ckpt8_used(rows: int, d: int) -> int:
 
 
 def lsq_ckpt8_pack(x, ckpt, rows: int, d: int, stream=None):
-    f, dev = "lsq_ckpt8_pack", _dev()
+    f = "lsq_ckpt8_pack"
+    dev, st = _here(stream)
     _call(f, _t(f, "x", x, torch.bfloat16, rows * d, dev), _t(f, "ckpt", ckpt, None, _ckpt8_used(rows, d), dev),
-          rows, d, _stream(stream))
+          rows, d, st)
 
 
 def lsq_ckpt8_unpack(ckpt, x, rows: int, d: int, stream=None):
-    f, dev = "lsq_ckpt8_unpack", _dev()
+    f = "lsq_ckpt8_unpack"
+    dev, st = _here(stream)
     _call(f, _t(f, "ckpt", ckpt, None, _ckpt8_used(rows, d), dev), _t(f, "x", x, torch.bfloat16, rows * d, dev),
-          rows, d, _stream(stream))
+          rows, d, st)
 
 
 def lsq_rmsnorm_fwd_pack8(x, g, y, rstd, ckpt, rows: int, d: int, eps: float, stream=None):
     """lsq_rmsnorm_fwd that also leaves x's 8-bit checkpoint."""
-    f, dev, n, bf = "lsq_rmsnorm_fwd_pack8", _dev(), rows * d, torch.bfloat16
+    f, n, bf = "lsq_rmsnorm_fwd_pack8", rows * d, torch.bfloat16
+    dev, st = _here(stream)
     _call(f, _t(f, "x", x, bf, n, dev), _t(f, "g", g, bf, d, dev), _t(f, "y", y, bf, n, dev),
           _t(f, "rstd", rstd, torch.float32, rows, dev), _t(f, "ckpt", ckpt, None, _ckpt8_used(rows, d), dev),
-          rows, d, eps, _stream(stream))
+          rows, d, eps, st)
 
 
 def lsq_rmsnorm_fwd_unpack8(ckpt, g, x, y, rstd, rows: int, d: int, eps: float, stream=None):
     """x restored from its 8-bit checkpoint, and lsq_rmsnorm_fwd of it."""
-    f, dev, n, bf = "lsq_rmsnorm_fwd_unpack8", _dev(), rows * d, torch.bfloat16
+    f, n, bf = "lsq_rmsnorm_fwd_unpack8", rows * d, torch.bfloat16
+    dev, st = _here(stream)
     _call(f, _t(f, "ckpt", ckpt, None, _ckpt8_used(rows, d), dev), _t(f, "g", g, bf, d, dev),
           _t(f, "x", x, bf, n, dev), _t(f, "y", y, bf, n, dev), _t(f, "rstd", rstd, torch.float32, rows, dev), rows, d,
-          eps, _stream(stream))
+          eps, st)
 
 
 def lsq_rmsnorm_bwd_unpack8(dy, ckpt, g, rstd, dres_in, dres_out, rows: int, d: int, stream=None):
     """lsq_rmsnorm_bwd with x read from its 8-bit checkpoint."""
-    f, dev, n, bf = "lsq_rmsnorm_bwd_unpack8", _dev(), rows * d, torch.bfloat16
+    f, n, bf = "lsq_rmsnorm_bwd_unpack8", rows * d, torch.bfloat16
+    dev, st = _here(stream)
     _call(f, _t(f, "dy", dy, bf, n, dev), _t(f, "ckpt", ckpt, None, _ckpt8_used(rows, d), dev),
           _t(f, "g", g, bf, d, dev), _t(f, "rstd", rstd, torch.float32, rows, dev),
-          _t(f, "dres_in", dres_in, bf, n, dev), _t(f, "dres_out", dres_out, bf, n, dev), rows, d, _stream(stream))
+          _t(f, "dres_in", dres_in, bf, n, dev), _t(f, "dres_out", dres_out, bf, n, dev), rows, d, st)
 
 
 def lsq_linear_fwd(x, w, bias, act: int, residual, z, y, M: int, N: int, K: int, stream=None):
     """y = residual + act(x w^T + bias); z receives the pre-activation; bias, residual and z may be None."""
-    f, dev, mn, bf = "lsq_linear_fwd", _dev(), M * N, torch.bfloat16
+    f, mn, bf = "lsq_linear_fwd", M * N, torch.bfloat16
+    dev, st = _here(stream)
     _call(f, _t(f, "x", x, bf, M * K, dev), _t(f, "w", w, bf, N * K, dev), _t(f, "bias", bias, bf, N, dev), act,
-          _t(f, "residual", residual, bf, mn, dev), _t(f, "z", z, bf, mn, dev), _t(f, "y", y, bf, mn, dev), M, N, K,
-          _stream(stream))
+          _t(f, "residual", residual, bf, mn, dev), _t(f, "z", z, bf, mn, dev), _t(f, "y", y, bf, mn, dev), M, N, K, st)
 
 
 def lsq_linear_bwd_workspace_size(M: int, N: int, K: int, act: int) -> int:
@@ -686,14 +698,14 @@ def lsq_linear_bwd_workspace_size(M: int, N: int, K: int, act: int) -> int:
 def lsq_linear_bwd(dy, x, w, z, act: int, dx, dw, dw_f32: int, dbias, accumulate: int, M: int, N: int, K: int,
                    workspace, stream=None):
     """dx, dw and dbias (each may be None) of lsq_linear_fwd from dy and the kept pre-activation z."""
-    f, dev, mn, bf, f32 = "lsq_linear_bwd", _dev(), M * N, torch.bfloat16, torch.float32
+    f, mn, bf, f32 = "lsq_linear_bwd", M * N, torch.bfloat16, torch.float32
+    dev, st = _here(stream)
     # at least: a tall dz pass adds a kernel for dbias
     launches = (1 if act != ACT_NONE or dbias is not None else 0) + (dx is not None) + (dw is not None)
     _call(f, _t(f, "dy", dy, bf, mn, dev), _t(f, "x", x, bf, M * K, dev), _t(f, "w", w, bf, N * K, dev),
           _t(f, "z", z, bf, mn, dev), act, _t(f, "dx", dx, bf, M * K, dev),
           _t(f, "dw", dw, f32 if dw_f32 else bf, N * K, dev), dw_f32, _t(f, "dbias", dbias, f32, N, dev), accumulate,
-          M, N, K, _t(f, "workspace", workspace, None, 0, dev), _nbytes(workspace), _stream(stream),
-          launches=launches)
+          M, N, K, _t(f, "workspace", workspace, None, 0, dev), _nbytes(workspace), st, launches=launches)
 
 
 # ---------------------------------------------------------------------------- streaming

@@ -89,6 +89,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int wh
   }
 }
 
+// After a wait on a ring of copies gave up at stage s: the copies still under way land before the block ends (one
+// more bounded wait each, in their order; the first that gives up again ends it).
+__device__ __forceinline__ void mbar_drain(uint64_t* full, int stages, int s, uint32_t parity, int where) {
+#pragma unroll 1
+  for (int i = 0; i < stages; ++i) {
+    if (!mbar_wait(&full[s], parity, where)) return;
+    if (++s == stages) s = 0, parity ^= 1;
+  }
+}
+
 // ---------------------------------------------------------------- programmatic launch
 // A kernel launched by launch_chained (host_common.h) may start while its predecessor on the stream still
 // runs: it sets up (shared memory, barriers, tensor memory), calls grid_wait before its first access to global

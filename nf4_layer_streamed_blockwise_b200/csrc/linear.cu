@@ -298,7 +298,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_
     int s = 0;
     uint32_t ph = 0;
     for (int i = kb0; i < kb1; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, 531))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, 531))) {
+        mbar_drain(full, C::NST, s, ph, 532);
+        break;
+      }
       tc_fence_after();
       const uint64_t at = (uint64_t)(s * (C::STAGE >> 4));
       if (elect_one()) {
@@ -509,6 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GTHREADS, 1)
         if (elect_one()) nf4g::tc_commit_pair(drain);
         __syncwarp();
         mbar_wait(drain, 0, 543);
+        mbar_drain(full, GST, s, ph, 544);
       }
     }
   } else {
@@ -948,20 +952,12 @@ extern "C" lsq_status lsq_linear_bwd(const void* dy, const void* x, const void* 
   if (pass && (!workspace || !aligned(workspace, 256) ||
                workspace_bytes < lsq_linear_bwd_workspace_size(M, N, K, act)))
     return fail(LSQ_EINVAL, "%s: workspace missing, misaligned or too small", who);
-  struct Range {
-    const void* p;
-    size_t n;
-  };
   const size_t mn = (size_t)M * N * 2, mk = (size_t)M * K * 2, nk = (size_t)N * K * 2;
-  const Range in[] = {{dy, mn}, {x, dw ? mk : 0}, {w, dx ? nk : 0}, {act != LSQ_ACT_NONE ? z : nullptr, mn}};
-  const Range out[] = {{dx, mk}, {dw, dw_f32 ? 2 * nk : nk}, {dbias, (size_t)N * 4},
-                       {pass ? workspace : nullptr, lsq_linear_bwd_workspace_size(M, N, K, act)}};
-  for (int i = 0; i < 4; ++i) {
-    for (const Range& r : in)
-      if (r.n && overlap(out[i].p, out[i].n, r.p, r.n)) return fail(LSQ_EINVAL, "%s: an output overlaps an input", who);
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return fail(LSQ_EINVAL, "%s: outputs overlap", who);
-  }
+  const nrm::Range in[] = {
+      {dy, mn}, {dw ? x : nullptr, mk}, {dx ? w : nullptr, nk}, {act != LSQ_ACT_NONE ? z : nullptr, mn}};
+  const nrm::Range out[] = {{dx, mk}, {dw, dw_f32 ? 2 * nk : nk}, {dbias, (size_t)N * 4},
+                            {pass ? workspace : nullptr, lsq_linear_bwd_workspace_size(M, N, K, act)}};
+  if (nrm::clash(out, in)) return fail(LSQ_EINVAL, "%s: overlapping arguments", who);
   if ((st = check_device()) != LSQ_OK) return st;
   if (pass && workspace_bytes < lsq_linear_bwd_workspace_size(M, N, K, act))  // now that the device's SMs are known
     return fail(LSQ_EINVAL, "%s: workspace too small for this device", who);

@@ -124,6 +124,9 @@ struct Ckpt {
   uint16_t* amax;   // bf16 [rows][ceil(d / 64)]
 };
 static size_t ckpt_amax_off(int64_t rows, int64_t d) { return (size_t)(rows * d + 15) / 16 * 16; }
+static size_t ckpt_used(int64_t rows, int64_t d) {
+  return ckpt_amax_off(rows, d) + (size_t)rows * (size_t)((d + 63) / 64) * 2;
+}
 static Ckpt ckpt_of(const void* p, int64_t rows, int64_t d) {
   uint8_t* b = static_cast<uint8_t*>(const_cast<void*>(p));
   return Ckpt{b, reinterpret_cast<uint16_t*>(b + ckpt_amax_off(rows, d))};
@@ -177,6 +180,19 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) row_fwd_kern
       if (c < d8) p.xo[base + c] = xv[i];
     }
   }
+  // short rows' gain and bias are under way with x, not behind the row's sums (one row of 4096: 1.6 us, not
+  // 1.8; with two words a thread the registers cost more: 8192 x 5120 39.5 us for 34.8)
+  constexpr bool AHEAD = NORM != NONE && V == 1;
+  uint4 gv[AHEAD ? V : 1], bv[AHEAD && NORM == LAYER ? V : 1];
+  auto gain = [&](int c) { return c < d8 ? p.g[c] : make_uint4(0u, 0u, 0u, 0u); };
+  auto bias = [&](int c) { return c < d8 && p.b ? p.b[c] : make_uint4(0u, 0u, 0u, 0u); };
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      gv[i] = gain(t + i * T);
+      if constexpr (NORM == LAYER) bv[i] = bias(t + i * T);
+    }
+  }
   if (PACK) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -219,8 +235,8 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) row_fwd_kern
       const int c = t + i * T;
       if (c >= d8) break;
       uint64_t g[4], b[4];
-      unpack_pairs(p.g[c], g);
-      unpack_pairs(p.b ? p.b[c] : make_uint4(0u, 0u, 0u, 0u), b);
+      unpack_pairs(AHEAD ? gv[AHEAD ? i : 0] : gain(c), g);
+      unpack_pairs(AHEAD ? bv[AHEAD ? i : 0] : bias(c), b);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[i][j] = fma2(mul2(f[i][j], rs2), g[j], b[j]);
       p.y[base + c] = pack_pairs(f[i]);
@@ -243,7 +259,7 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) row_fwd_kern
       if (c >= d8) break;
       uint64_t f[4], g[4];
       unpack_pairs(xv[i], f);
-      unpack_pairs(p.g[c], g);
+      unpack_pairs(AHEAD ? gv[AHEAD ? i : 0] : gain(c), g);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[j] = mul2(mul2(f[j], f2(rs, rs)), g[j]);
       p.y[base + c] = pack_pairs(f);
@@ -414,6 +430,7 @@ template <int V, bool GRADS>
 __global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_constant__ Bwd p, int nst, int stage, int cs) {
   extern __shared__ __align__(128) uint8_t smem[];  // per warp [nst][x | dy | res], then every stage's barrier
   __shared__ float comb[LNW * 32 * 9];
+  __shared__ int gave_up[LNW];  // stage and parity of a wait that did (in registers it costs the loop 1%)
   __shared__ float4 xs[GRADS ? 2 * V * 64 : 1];  // this block's sums, for ln_join_sums
   const int t = (int)(threadIdx.x & 31), w = (int)(threadIdx.x >> 5);
   uint8_t* ring = smem + (size_t)w * nst * stage;
@@ -442,10 +459,10 @@ __global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_c
   }
   int s = 0;
   uint32_t ph = 0;
-  bool ok = true;  // after a wait that gave up, the rest of the rows is not waited for
+  bool ok = true;  // after a wait that gave up, the rest of the rows is neither fetched nor waited for
   for (int64_t row = first; row < p.rows; row += step) {
     const float mu = p.mean[row], r = p.rstd[row];
-    if (ok) ok = mbar_wait(&full[s], ph, 461);
+    if (ok && !(ok = mbar_wait(&full[s], ph, 461)) && t == 0) gave_up[w] = 2 * s + (int)ph;
     const uint4* b = reinterpret_cast<const uint4*>(ring + (size_t)s * stage);
     const uint64_t nmu = f2(-mu, -mu), rs = f2(r, r);
     uint64_t xh[4], a[4], s1 = 0ull, s2 = 0ull;
@@ -466,10 +483,11 @@ __global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_c
       p.out[row * d8 + c] = ln_bwd_out(xh, a, p.res ? b[2 * d8 + c] : z, rs, f2(k1, k1), f2(k2, k2));
     }
     __syncwarp();  // the warp is done with the stage: refill it
-    if (t == 0 && row + nst * step < p.rows)
+    if (t == 0 && ok && row + nst * step < p.rows)
       ln_fetch(p, ring + (size_t)s * stage, &full[s], rb, row + nst * step);
     if (++s == nst) s = 0, ph ^= 1;
   }
+  if (!ok && t == 0) mbar_drain(full, nst, gave_up[w] >> 1, (uint32_t)gave_up[w] & 1u, 462);
   if constexpr (GRADS) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -505,6 +523,7 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
     ln_bwd_block_kernel(const __grid_constant__ Bwd p, int nst, int stage, int cs) {
   extern __shared__ __align__(128) uint8_t ring[];  // [nst][x | dy | res], then the stages' barriers
   __shared__ float2 red[2][16];
+  __shared__ int gave_up;
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)nst * stage);
   const int T = (int)blockDim.x, t = (int)threadIdx.x, d8 = p.d8, nw = T >> 5, lane = t & 31;
   const uint32_t rb = (uint32_t)d8 * 16;
@@ -530,10 +549,10 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
   }
   int s = 0, flip = 0;
   uint32_t ph = 0;
-  bool ok = true;  // after a wait that gave up, the rest of the rows is not waited for
+  bool ok = true;  // after a wait that gave up, the rest of the rows is neither fetched nor waited for
   for (int64_t row = first; row < p.rows; row += step, flip ^= 1) {
     const float mu = p.mean[row], r = p.rstd[row];
-    if (ok) ok = mbar_wait(&full[s], ph, 461);
+    if (ok && !(ok = mbar_wait(&full[s], ph, 461)) && t == 0) gave_up = 2 * s + (int)ph;
     const uint4* b = reinterpret_cast<const uint4*>(ring + (size_t)s * stage);
     const uint64_t nmu = f2(-mu, -mu), rs = f2(r, r);
     uint64_t xh[4], a[4], s1 = 0ull, s2 = 0ull;
@@ -548,7 +567,7 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
     const float w1 = warp_sum(pair_sum(s1)), w2 = warp_sum(pair_sum(s2));
     if (lane == 0) red[flip][t >> 5] = make_float2(w1, w2);
     __syncthreads();
-    if (t == 0 && row != first) {  // the previous row's stage
+    if (t == 0 && ok && row != first) {  // the previous row's stage
       const int64_t next = row + (nst - 1) * step;
       const int prev = s == 0 ? nst - 1 : s - 1;
       if (next < p.rows) ln_fetch(p, ring + (size_t)prev * stage, &full[prev], rb, next);
@@ -571,6 +590,7 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
     }
     if (++s == nst) s = 0, ph ^= 1;
   }
+  if (!ok && t == 0) mbar_drain(full, nst, gave_up >> 1, (uint32_t)gave_up & 1u, 462);
   if constexpr (GRADS) {
     float4* xs = reinterpret_cast<float4*>(ring);  // in place of the ring
     if (cs > 1) __syncthreads();
@@ -641,10 +661,12 @@ lsq_status col_sum(const float* part, int G, int64_t ld, int64_t n0, int64_t nco
 }
 
 // ---------------------------------------------------------------- geometry
-// WARP rows up to d = 1024 (V words a lane); block rows with V words a thread.  Few rows: one word a thread
-// (the row's latency decides).  Many, for 8192 x 5120 with 1 / 2 / 4 words: norm and checkpoint 46.7 / 35.0 /
-// 36.4 us, restore and norm 42.7 / 34.2 / 34.9; LayerNorm's two reductions a row ask for fewer threads in each
-// (46.7 / 37.8 / 31.7), the backward's three arrays for fewer registers (50.8 / 57.9 / 60.3).
+// WARP rows up to d = 1024 (V words a lane); block rows with V words a thread.  One word a thread (the row's
+// latency decides) while the rows run in about one round: norm and checkpoint of 1000 x 2048 3.1 us with one
+// word, 4.3 with two; 1500 x 2048 (1.3 rounds) 3.8 and 4.4, 700 x 5120 (1.5) 4.7 and 4.5; LayerNorm of
+// 600 x 4096 (1.0) 3.8 and 3.7 with four.  More rows, for 8192 x 5120 with 1 / 2 / 4 words: norm and checkpoint
+// 46.7 / 35.0 / 36.4 us, restore and norm 42.7 / 34.2 / 34.9; LayerNorm's two reductions a row ask for fewer
+// threads in each (46.7 / 37.8 / 31.7), the backward's three arrays for fewer registers (50.8 / 57.9 / 60.3).
 enum Pass { FORWARD, LAYERNORM, BACKWARD };
 struct Geo {
   int v, threads, warp;
@@ -660,7 +682,9 @@ static Geo row_geo(int64_t rows, int d8, Pass pass) {
     g.blocks = (unsigned)((rows + per - 1) / per);
     return g;
   }
-  const bool many = rows >= 2 * num_sms() && pass != BACKWARD;
+  const int64_t round = 2048ll * num_sms();  // threads that run at once
+  const bool many =
+      rows >= 2 * num_sms() && (pass == LAYERNORM ? rows * d8 > round : pass == FORWARD && 3 * rows * d8 > 4 * round);
   g.v = d8 > 1024 ? (many ? 4 : 2) : many && d8 >= 512 && pass == LAYERNORM ? 4 : many && d8 >= 256 ? 2 : 1;
   g.threads = (((d8 + g.v - 1) / g.v) + 31) / 32 * 32;
   g.blocks = (unsigned)rows;
@@ -758,6 +782,25 @@ template <typename... P>
 static bool aligned16(P... p) {
   return (... && aligned(p, 16));
 }
+template <typename... P>
+static bool aligned4(P... p) {
+  return (... && aligned(p, 4));
+}
+struct Range {
+  const void* p;  // null: none
+  size_t n;
+};
+// an output shares bytes with an input or another output
+template <size_t O, size_t I>
+static bool clash(const Range (&out)[O], const Range (&in)[I]) {
+  for (size_t i = 0; i < O; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i].p, out[i].n, r.p, r.n)) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
 // an output over its input's bytes at another place: a row would be written before another reads it
 static bool shifted(const void* in, const void* out, size_t bytes) {
   return in != out && overlap(in, bytes, out, bytes);
@@ -774,8 +817,10 @@ extern "C" lsq_status lsq_layernorm_fwd(const void* x, const void* g, const void
   if (!x || !g || !y) return fail(LSQ_EINVAL, "%s: NULL argument", who);
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
-  if (!nrm::aligned16(x, g, b, y)) return fail(LSQ_EINVAL, "%s: alignment", who);
-  if (nrm::shifted(x, y, (size_t)rows * d * 2)) return fail(LSQ_EINVAL, "%s: y overlaps x", who);
+  if (!nrm::aligned16(x, g, b, y) || !nrm::aligned4(mean, rstd)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  const size_t xb = (size_t)rows * d * 2, gb = (size_t)d * 2, sb = (size_t)rows * 4;
+  const nrm::Range out[] = {{y, xb}, {mean, sb}, {rstd, sb}}, in[] = {{x == y ? nullptr : x, xb}, {g, gb}, {b, gb}};
+  if (nrm::clash(out, in)) return fail(LSQ_EINVAL, "%s: overlapping arguments (y may be x itself)", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Fwd p{};
   p.x = (const uint4*)x;
@@ -802,13 +847,19 @@ extern "C" lsq_status lsq_layernorm_bwd(const void* dy, const void* x, const voi
   if (!dy || !x || !g || !mean || !rstd || !dres_out) return fail(LSQ_EINVAL, "%s: NULL argument", who);
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
-  if (!nrm::aligned16(dy, x, g, dres_in, dres_out, dg, db)) return fail(LSQ_EINVAL, "%s: alignment", who);
-  const size_t xb = (size_t)rows * d * 2;
-  if (nrm::shifted(dy, dres_out, xb) || nrm::shifted(x, dres_out, xb) || nrm::shifted(dres_in, dres_out, xb))
-    return fail(LSQ_EINVAL, "%s: dres_out overlaps an input", who);
+  if (!nrm::aligned16(dy, x, g, dres_in, dres_out, dg, db) || !nrm::aligned4(mean, rstd))
+    return fail(LSQ_EINVAL, "%s: alignment", who);
+  const size_t xb = (size_t)rows * d * 2, gb = (size_t)d * 4, sb = (size_t)rows * 4;
   const bool grads = dg || db;
-  if (grads && (!workspace || !aligned(workspace, 256) || workspace_bytes < lsq_layernorm_bwd_workspace_size(rows, d)))
+  const size_t wb = grads ? lsq_layernorm_bwd_workspace_size(rows, d) : 0;
+  if (grads && (!workspace || !aligned(workspace, 256) || workspace_bytes < wb))
     return fail(LSQ_EINVAL, "%s: workspace missing, misaligned or too small", who);
+  auto in_place = [&](const void* v) { return v == dres_out ? nullptr : v; };
+  const nrm::Range out[] = {{dres_out, xb}, {dg, gb}, {db, gb}, {grads ? workspace : nullptr, wb}};
+  const nrm::Range in[] = {{in_place(dy), xb}, {in_place(x), xb}, {in_place(dres_in), xb},
+                           {g, gb / 2},        {mean, sb},        {rstd, sb}};
+  if (nrm::clash(out, in))
+    return fail(LSQ_EINVAL, "%s: overlapping arguments (dres_out may be dy, x or dres_in itself)", who);
   if ((st = check_device()) != LSQ_OK) return st;
   if (grads && workspace_bytes < lsq_layernorm_bwd_workspace_size(rows, d))  // now that the device's SMs are known
     return fail(LSQ_EINVAL, "%s: workspace too small for this device", who);
@@ -843,7 +894,7 @@ extern "C" lsq_status lsq_layernorm_bwd(const void* dy, const void* x, const voi
 // ---------------------------------------------------------------- 8-bit checkpoints
 extern "C" size_t lsq_ckpt8_size(int64_t rows, int64_t d) {
   if (rows < 1 || d < 1) return 256;
-  return (nrm::ckpt_amax_off(rows, d) + (size_t)rows * (size_t)((d + 63) / 64) * 2 + 255) / 256 * 256;
+  return (nrm::ckpt_used(rows, d) + 255) / 256 * 256;
 }
 
 extern "C" lsq_status lsq_ckpt8_pack(const void* x, void* ckpt, int64_t rows, int64_t d, lsq_cuda_stream stream) {
@@ -852,7 +903,7 @@ extern "C" lsq_status lsq_ckpt8_pack(const void* x, void* ckpt, int64_t rows, in
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
   if (!nrm::aligned16(x, ckpt)) return fail(LSQ_EINVAL, "%s: alignment", who);
-  if (overlap(x, (size_t)rows * d * 2, ckpt, lsq_ckpt8_size(rows, d)))
+  if (overlap(x, (size_t)rows * d * 2, ckpt, nrm::ckpt_used(rows, d)))
     return fail(LSQ_EINVAL, "%s: x overlaps the checkpoint", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Fwd p{};
@@ -867,7 +918,7 @@ extern "C" lsq_status lsq_ckpt8_unpack(const void* ckpt, void* x, int64_t rows, 
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
   if (!nrm::aligned16(x, ckpt)) return fail(LSQ_EINVAL, "%s: alignment", who);
-  if (overlap(x, (size_t)rows * d * 2, ckpt, lsq_ckpt8_size(rows, d)))
+  if (overlap(x, (size_t)rows * d * 2, ckpt, nrm::ckpt_used(rows, d)))
     return fail(LSQ_EINVAL, "%s: x overlaps the checkpoint", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Fwd p{};
@@ -882,10 +933,11 @@ extern "C" lsq_status lsq_rmsnorm_fwd_pack8(const void* x, const void* g, void* 
   if (!x || !g || !y || !ckpt) return fail(LSQ_EINVAL, "%s: NULL argument", who);
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
-  if (!nrm::aligned16(x, g, y, ckpt)) return fail(LSQ_EINVAL, "%s: alignment", who);
-  const size_t xb = (size_t)rows * d * 2, cb = lsq_ckpt8_size(rows, d);
-  if (nrm::shifted(x, y, xb) || overlap(x, xb, ckpt, cb) || overlap(y, xb, ckpt, cb))
-    return fail(LSQ_EINVAL, "%s: overlapping arguments", who);
+  if (!nrm::aligned16(x, g, y, ckpt) || !nrm::aligned4(rstd)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  const size_t xb = (size_t)rows * d * 2, cb = nrm::ckpt_used(rows, d);
+  const nrm::Range out[] = {{y, xb}, {rstd, (size_t)rows * 4}, {ckpt, cb}};
+  const nrm::Range in[] = {{x == y ? nullptr : x, xb}, {g, (size_t)d * 2}};
+  if (nrm::clash(out, in)) return fail(LSQ_EINVAL, "%s: overlapping arguments (y may be x itself)", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Fwd p{};
   p.x = (const uint4*)x;
@@ -903,10 +955,11 @@ extern "C" lsq_status lsq_rmsnorm_fwd_unpack8(const void* ckpt, const void* g, v
   if (!x || !g || !y || !ckpt) return fail(LSQ_EINVAL, "%s: NULL argument", who);
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
-  if (!nrm::aligned16(x, g, y, ckpt)) return fail(LSQ_EINVAL, "%s: alignment", who);
-  const size_t xb = (size_t)rows * d * 2, cb = lsq_ckpt8_size(rows, d);
-  if (overlap(x, xb, y, xb) || overlap(x, xb, ckpt, cb) || overlap(y, xb, ckpt, cb))
-    return fail(LSQ_EINVAL, "%s: overlapping arguments", who);
+  if (!nrm::aligned16(x, g, y, ckpt) || !nrm::aligned4(rstd)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  const size_t xb = (size_t)rows * d * 2;
+  const nrm::Range out[] = {{x, xb}, {y, xb}, {rstd, (size_t)rows * 4}};
+  const nrm::Range in[] = {{ckpt, nrm::ckpt_used(rows, d)}, {g, (size_t)d * 2}};
+  if (nrm::clash(out, in)) return fail(LSQ_EINVAL, "%s: overlapping arguments", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Fwd p{};
   p.in = nrm::ckpt_of(ckpt, rows, d);
@@ -926,11 +979,17 @@ extern "C" lsq_status lsq_rmsnorm_bwd_unpack8(const void* dy, const void* ckpt, 
   if (!dy || !ckpt || !g || !rstd || !dres_out) return fail(LSQ_EINVAL, "%s: NULL argument", who);
   lsq_status st = nrm::check_rows(who, rows, d);
   if (st != LSQ_OK) return st;
-  if (!nrm::aligned16(dy, ckpt, g, dres_in, dres_out)) return fail(LSQ_EINVAL, "%s: alignment", who);
+  if (!nrm::aligned16(dy, ckpt, g, dres_in, dres_out) || !nrm::aligned4(rstd))
+    return fail(LSQ_EINVAL, "%s: alignment", who);
   const size_t xb = (size_t)rows * d * 2;
-  if (nrm::shifted(dy, dres_out, xb) || nrm::shifted(dres_in, dres_out, xb) ||
-      overlap(dres_out, xb, ckpt, lsq_ckpt8_size(rows, d)))
-    return fail(LSQ_EINVAL, "%s: dres_out overlaps an input", who);
+  const nrm::Range out[] = {{dres_out, xb}};
+  const nrm::Range in[] = {{dy == dres_out ? nullptr : dy, xb},
+                           {dres_in == dres_out ? nullptr : dres_in, xb},
+                           {ckpt, nrm::ckpt_used(rows, d)},
+                           {g, (size_t)d * 2},
+                           {rstd, (size_t)rows * 4}};
+  if (nrm::clash(out, in))
+    return fail(LSQ_EINVAL, "%s: overlapping arguments (dres_out may be dy or dres_in itself)", who);
   if ((st = check_device()) != LSQ_OK) return st;
   nrm::Bwd p{};
   p.dy = (const uint4*)dy;

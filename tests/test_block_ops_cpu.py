@@ -130,3 +130,52 @@ def test_sizes():
     assert L.lsq_ckpt8_size(3, 72) == 256 and L.lsq_ckpt8_size(2048, 4096) == 2048 * 4096 + 2048 * 64 * 2
     assert L.lsq_layernorm_bwd_workspace_size(1, 64) % 256 == 0
     assert L.lsq_linear_bwd_workspace_size(128, 256, 64, 0) < L.lsq_linear_bwd_workspace_size(128, 256, 64, 1)
+
+
+# the row passes' other overlaps: call, arguments, pairs of an output and the argument whose place it is given
+OVERLAPS = {
+    "ln_fwd": (L.lsq_layernorm_fwd, [*_at(6), 4, 64, 1e-5],
+               [(3, 1), (3, 2), (4, 0), (4, 1), (4, 2), (4, 3), (5, 0), (5, 3), (5, 4)]),
+    "fwd_pack8": (L.lsq_rmsnorm_fwd_pack8, [*_at(5), 4, 64, 1e-5], [(2, 1), (3, 0), (3, 1), (3, 2), (3, 4), (4, 1)]),
+    "fwd_unpack8": (L.lsq_rmsnorm_fwd_unpack8, [*_at(5), 4, 64, 1e-5], [(2, 1), (3, 1), (4, 0), (4, 1), (4, 2), (4, 3)]),
+    "bwd_unpack8": (L.lsq_rmsnorm_bwd_unpack8, [*_at(6), 4, 64], [(5, 2), (5, 3)]),
+}
+
+
+@pytest.mark.parametrize("name", sorted(OVERLAPS))
+def test_row_passes_refuse_every_overlap(name):
+    fn, args, pairs = OVERLAPS[name]
+    for out, other in pairs:
+        _refused(EINVAL, fn, *[args[other] if k == out else v for k, v in enumerate(args)])
+
+
+def test_statistics_are_aligned():
+    for name, at in (("ln_fwd", 4), ("ln_fwd", 5), ("fwd_pack8", 3), ("fwd_unpack8", 4), ("bwd_unpack8", 3)):
+        fn, args, _ = OVERLAPS[name]
+        _refused(EINVAL, fn, *[v + 2 if k == at else v for k, v in enumerate(args)])
+
+
+def test_layernorm_backward_refuses_every_overlap():
+    """dy x g mean rstd dres_in dres_out dg db, then the workspace."""
+    fn, need = L._fn("lsq_layernorm_bwd"), L.lsq_layernorm_bwd_workspace_size(4, 64)
+    a = _at(10)
+    for out, others in ((6, (2, 3, 4)), (7, (0, 1, 2, 3, 4, 5, 6)), (8, (0, 1, 2, 3, 4, 5, 6, 7)), (9, range(9))):
+        for other in others:
+            v = list(a)
+            v[out] = v[other]
+            assert fn(*v[:9], 0, 4, 64, v[9], need, S) == EINVAL, (out, other)
+    for k in (3, 4):
+        v = list(a)
+        v[k] += 2
+        assert fn(*v[:9], 0, 4, 64, v[9], need, S) == EINVAL, k
+
+
+def test_linear_backward_refuses_every_overlap():
+    """dy x w z dx dw dbias, then the workspace."""
+    fn, need = L._fn("lsq_linear_bwd"), L.lsq_linear_bwd_workspace_size(4, 64, 64, 2)
+    a = _at(8)
+    for out, others in ((4, (0, 1, 2, 3)), (5, (0, 1, 2, 3, 4)), (6, (0, 1, 2, 3, 4, 5)), (7, range(7))):
+        for other in others:
+            v = list(a)
+            v[out] = v[other]
+            assert fn(*v[:4], 2, v[4], v[5], 1, v[6], 0, 4, 64, 64, v[7], need, S) == EINVAL, (out, other)

@@ -142,3 +142,10 @@ def test_size_is_what_is_written(lsq):
     lsq.lsq_ckpt8_pack(_x(rows, d).cuda(), buf, rows, d)
     used = -(-rows * d // 16) * 16 + rows * 2 * 2
     assert used <= size and (buf[used:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("rows,d", [(1000, 4104), (1580, 2048), (1578, 2048), (400, 8200), (390, 8328)])
+def test_more_rows_than_run_at_once(lsq, rows, d):
+    """Two and four words a thread, and both sides of where they begin."""
+    test_bit_exact(lsq, rows, d)
+    test_fused_passes_equal_their_parts(lsq, rows, d)

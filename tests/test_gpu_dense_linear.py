@@ -188,3 +188,56 @@ def test_rows_behind_the_last_are_left_alone(lsq):
     lsq.lsq_linear_bwd(t["dy"], t["x"], t["w"], z, 2, dx, dw, 1, db, 0, M, N, K, ws)
     for u, n in ((y, M), (z, M), (dx, M), (dw, N), (db, N)):
         assert (u[n:] == 7).all() and not (u[:n] == 7).all()
+
+
+def test_after_copies_and_joins_in_a_graph(lsq):
+    """Calls captured behind a copy, a fill and the join of another stream, which are no kernels of this library:
+    each waits for all of them, in the graph's replays as in the eager run."""
+    M, N, K = 96, 264, 520
+    g = torch.Generator(device="cuda").manual_seed(5)
+    src = [torch.randn(M, K, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2)]
+    w = torch.randn(N, K, device="cuda", generator=g).to(torch.bfloat16)
+    big = torch.randn(64, 1 << 20, device="cuda", generator=g)      # keeps the other stream busy for a while
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    y, y2, dw = (torch.empty(s, dtype=t, device="cuda") for s, t in
+                 (((M, N), torch.bfloat16), ((M, N), torch.bfloat16), ((N, K), torch.float32)))
+    staged = torch.empty_like(src[0])
+    side = torch.cuda.Stream()
+
+    def run():
+        cur = torch.cuda.current_stream()
+        x.copy_(staged)                                              # a copy node, then a kernel that reads it
+        lsq.lsq_linear_fwd(x, w, None, 0, None, None, y, M, N, K)
+        dw.zero_()                                                   # a fill, then a kernel that adds to it
+        lsq.lsq_linear_bwd(y, x, w, None, 0, None, dw, 1, None, 1, M, N, K, None)
+        side.wait_stream(cur)
+        with torch.cuda.stream(side):
+            big.mul_(1.0)
+            x.mul_(2.0)
+        cur.wait_stream(side)                                        # the join, then a kernel that reads it
+        lsq.lsq_linear_fwd(x, w, None, 0, None, None, y2, M, N, K)
+
+    want = []
+    for s in src:
+        staged.copy_(s)
+        run()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (y, dw, y2)])
+    cap = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=cap):
+        run()
+    for _ in range(3):
+        for s, w0 in zip(src, want):
+            staged.copy_(s)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            for got, ref in zip((y, dw, y2), w0):
+                assert torch.equal(got, ref)
+    for s, (y0, dw0, y20) in zip(src, want):                         # and the eager results are the products
+        ref = s.double() @ w.double().t()
+        assert (y0.double() - ref).norm() <= 2 ** -8 * ref.norm()
+        assert (y20.double() - 2 * ref).norm() <= 2 ** -8 * (2 * ref).norm()
+        ref = y0.double().t() @ s.double()
+        assert (dw0.double() - ref).norm() <= 2e-5 * ref.norm()

@@ -169,3 +169,10 @@ def test_in_place(lsq, rows, d):
     b = t["x"].clone()
     for got in (bwd(a, t["x"], a), bwd(t["dy"], b, b)):
         assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("rows,d", [(1300, 2056), (1185, 2048), (1184, 2048), (2000, 2304)])
+@pytest.mark.parametrize("bias", [True, False])
+def test_forward_of_more_rows_than_run_at_once(lsq, rows, d, bias):
+    """Two words a thread (the other widths are among the shapes above), and both sides of where it begins."""
+    test_forward(lsq, rows, d, bias)

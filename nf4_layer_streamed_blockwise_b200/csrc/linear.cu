@@ -12,7 +12,7 @@
 //   dW       p = k, q = n, c = m:  P = x  MN-major,  Q = dz MN-major
 //
 // Two forms share them (one row's forward has a third): one tile per cluster with the contraction split (few
-// tiles: bound by what L2 feeds an SM, and below that by start and exchange)
+// tiles: bound by what L2 feeds an SM, and below that by start and exchange; dx and dW share a launch there)
 // and a persistent CTA-pair form (many tiles: bound by the tensor cores, in a
 // long run by the power cap); plan_product picks by a measured cost model.
 // Measured on B200 (graph replays): 2048 x 14336 x 4096 forward 153-156 us with
@@ -232,19 +232,19 @@ struct Cfg {
 };
 
 template <int PMN, int QMN, int BT>
-__global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_constant__ Maps maps,
-                                                                   const __grid_constant__ Params p) {
+__device__ __forceinline__ void split_tile(const Maps& maps, const Params& p, int block, uint8_t* smem_raw) {
   using C = Cfg<BT>;
-  extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NST;
   uint64_t* afull = empty + C::NST;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = p.splits, rank = (int)(blockIdx.x % S), tile = (int)(blockIdx.x / S);
+  const int S = p.splits, rank = block % S, tile = block / S;
   const int p0 = (tile % p.tp) * BP, q0 = (tile / p.tp) * BT;
-  const int kb0 = (int)((int64_t)p.nkb * rank / S), kb1 = (int)((int64_t)p.nkb * (rank + 1) / S);
+  const int kb0 = (int)((int64_t)p.nkb * rank / S);
+  const int kb1 = q0 < p.Q ? (int)((int64_t)p.nkb * (rank + 1) / S) : kb0;  // else a block that fills up a cluster
+  const int first = (int)nf4g::cluster_ctarank() - rank;  // the tile's first CTA: a cluster may hold several tiles
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_
   if (warp < 4) {
     const bool ok = __all_sync(0xffffffffu, mbar_wait(afull, 0, 731));
     tc_fence_after();
-    if (ok) {
+    if (ok && kb1 > kb0) {
       const uint32_t lb = tmem + ((uint32_t)(warp * 32) << 16);
       // row r of the tile is finished by rank r >> lper, as its row r & (per - 1).  Rolled: the code runs once
       // per block, so what counts is the instructions fetched (unrolled eightfold 333 x 1536 x 576 took 19.1
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_
         for (int t = 0; t < 16; ++t) {
           const uint32_t dst = mine + (uint32_t)(((c + t) & (per - 1)) * (BP * 4));
           uint32_t a;
-          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(dst), "r"((c + t) >> lper));
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(dst), "r"(first + ((c + t) >> lper)));
           asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v[t]) : "memory");
         }
       }
@@ -371,6 +371,26 @@ __global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_
     }
     finish8(v, p.e, (int64_t)q * p.P + col, col);
   }
+}
+
+template <int PMN, int QMN, int BT>
+__global__ void __launch_bounds__(NTHREADS, 1) linear_split_kernel(const __grid_constant__ Maps maps,
+                                                                   const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  split_tile<PMN, QMN, BT>(maps, p, (int)blockIdx.x, smem_raw);
+}
+
+// dx and dW of a small linear in one launch: the first blocks are dx's, the rest dW's, side by side in one round
+struct Both {
+  Maps mx, mw;
+  Params x, w;
+  int nx;  // blocks of dx
+};
+template <int BX, int BW>
+__global__ void __launch_bounds__(NTHREADS, 1) linear_both_kernel(const __grid_constant__ Both b) {
+  extern __shared__ uint8_t smem_raw[];
+  if ((int)blockIdx.x < b.nx) split_tile<1, 0, BX>(b.mx, b.x, (int)blockIdx.x, smem_raw);
+  else split_tile<1, 1, BW>(b.mw, b.w, (int)blockIdx.x - b.nx, smem_raw);
 }
 
 // ---------------------------------------------------------------- persistent form
@@ -720,45 +740,67 @@ static lsq_status launch_split(const Maps& maps, const Params& p, int64_t cluste
 //    no multiple of the 64-wide boxes loads columns that it does not use, 0.05 more.  Narrower tiles pay where
 //    they fill the last round: 2048 x 14336 x 4096 takes 159.6 with 224 columns (6.9 rounds of 74 pairs), 166.2
 //    with 256 (6.05); 512 x 4096 x 4096 18.6 with 128, 24.8 with 256 (one cluster a tile: 22.2).
+// 64-deep blocks of a contraction; the tail reads as zeros (TMA out-of-bounds fill)
+static int kblocks(int64_t C) { return (int)((C + BK - 1) / BK); }
 struct Plan {
   int pair, bt, splits, bn;
+  double us;
 };
+static double split_us(int bt, int nkb, int S) {
+  return (0.16 + 0.0006 * bt) * ((nkb + S - 1) / S) + 3.9 + 0.02 * bt;
+}
+// CTAs in clusters of S that run at once: clusters do not straddle GPCs
+static double split_fit(int S, int sms) { return S <= 2 ? sms : S == 4 ? sms - sms / 9 : sms - sms / 7; }
 static Plan plan_product(int64_t P, int64_t Q, int nkb, int pmn, int qmn) {
-  const double sms = num_sms();
+  const int sms = num_sms();
   Plan best{};
   double tb = 1e30;
   const int64_t tp = (P + BP - 1) / BP;
   for (int bt = qmn ? 64 : 16; bt <= 128; bt *= 2) {
     const double tiles = (double)(tp * ((Q + bt - 1) / bt));
     for (int S = 1; S <= MAX_S && S <= nkb; S *= 2) {
-      const double fit = S <= 2 ? sms : S == 4 ? sms - sms / 9 : sms - sms / 7;  // clusters do not straddle GPCs
-      const double t = std::ceil(tiles * S / fit) * ((0.16 + 0.0006 * bt) * ((nkb + S - 1) / S) + 3.9 + 0.02 * bt);
-      if (t < tb) tb = t, best = Plan{0, bt, S, 0};
+      const double t = std::ceil(tiles * S / split_fit(S, sms)) * split_us(bt, nkb, S);
+      if (t < tb) tb = t, best = Plan{0, bt, S, 0, t};
     }
   }
   for (int bn = 256; bn >= 128; bn -= 32) {
-    const double rounds = std::ceil((double)(((Q + TM - 1) / TM) * ((P + bn - 1) / bn)) / (sms / 2));
+    const double rounds = std::ceil((double)(((Q + TM - 1) / TM) * ((P + bn - 1) / bn)) / (sms / 2.0));
     const double prod = nkb * (std::max(0.235, 0.345 * bn / 256) + (pmn && bn / 2 % 64 ? 0.05 : 0.0));
     const double epi = 0.3 + 1.55 * bn / 256;
     const double t = 4.5 + rounds * (std::max(prod, epi) + 0.2 * std::min(prod, epi));
-    if (t < tb) tb = t, best = Plan{1, 0, 0, bn};
+    if (t < tb) tb = t, best = Plan{1, 0, 0, bn, t};
   }
   return best;
 }
 
+// Maps and parameters of the split form's tiles, for a plan
+static lsq_status split_args(Maps* maps, Params* p, const void* pop, int pmn, const void* qop, int qmn, int64_t P,
+                             int64_t Q, int64_t C, int bt, int splits, const Epi& e) {
+  memset(maps, 0, sizeof(*maps));
+  *p = Params{};
+  p->P = (int)P;
+  p->Q = (int)Q;
+  p->nkb = kblocks(C);
+  p->tp = (int)((P + BP - 1) / BP);
+  p->e = e;
+  p->splits = splits;
+  p->lper = (bt == 16 ? 4 : bt == 32 ? 5 : bt == 64 ? 6 : 7) - (splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3);
+  lsq_status st = map_operand(&maps->p, pop, pmn, P, C, BP);
+  if (st == LSQ_OK) st = map_operand(&maps->q, qop, qmn, Q, C, bt);
+  return st;
+}
+
 // out[Q, P] = sum over C of the operands (see the top), with the epilogue e
 template <int PMN, int QMN>
-static lsq_status product(const void* pop, const void* qop, int64_t P, int64_t Q, int64_t C, const Epi& e,
-                          cudaStream_t stream) {
+static lsq_status product(const Plan& plan, const void* pop, const void* qop, int64_t P, int64_t Q, int64_t C,
+                          const Epi& e, cudaStream_t stream) {
   Params p{};
-  p.P = (int)P;
-  p.Q = (int)Q;
-  p.nkb = (int)((C + BK - 1) / BK);  // the tail reads as zeros (TMA out-of-bounds fill)
-  p.tp = (int)((P + BP - 1) / BP);
-  p.e = e;
-  const Plan plan = plan_product(P, Q, p.nkb, PMN, QMN);
   lsq_status st;
   if (plan.pair) {
+    p.P = (int)P;
+    p.Q = (int)Q;
+    p.nkb = kblocks(C);
+    p.e = e;
     p.bn = plan.bn;
     GMaps gm;
     memset(&gm, 0, sizeof(gm));
@@ -779,21 +821,72 @@ static lsq_status product(const void* pop, const void* qop, int64_t P, int64_t Q
     return launch_pair<QMN, PMN, 0>(gm, p, tiles, stream);
   }
   const int bt = plan.bt;
-  p.splits = plan.splits;
-  p.lper = (bt == 16 ? 4 : bt == 32 ? 5 : bt == 64 ? 6 : 7) -
-           (p.splits == 1 ? 0 : p.splits == 2 ? 1 : p.splits == 4 ? 2 : 3);
-  const int64_t tiles = (int64_t)p.tp * ((Q + bt - 1) / bt);
   Maps maps;
-  memset(&maps, 0, sizeof(maps));
-  st = map_operand(&maps.p, pop, PMN, P, C, BP);
-  if (st == LSQ_OK) st = map_operand(&maps.q, qop, QMN, Q, C, bt);
-  if (st != LSQ_OK) return st;
+  if ((st = split_args(&maps, &p, pop, PMN, qop, QMN, P, Q, C, bt, plan.splits, e)) != LSQ_OK) return st;
+  const int64_t tiles = (int64_t)p.tp * ((Q + bt - 1) / bt);
   if constexpr (!QMN) {
     if (bt == 16) return launch_split<PMN, QMN, 16>(maps, p, tiles, stream);
     if (bt == 32) return launch_split<PMN, QMN, 32>(maps, p, tiles, stream);
   }
   if (bt == 64) return launch_split<PMN, QMN, 64>(maps, p, tiles, stream);
   return launch_split<PMN, QMN, 128>(maps, p, tiles, stream);
+}
+
+// dx [M, K] and dW [N, K] in one launch where both fit one round of the split form side by side and that is
+// estimated shorter than one after the other (the two products together and apart, graph replays: 130 x 576 x 1536
+// 6.7 us for 8.5, 256 x 1024 x 1024 7.1 for 9.6, 1000 x 1000 x 1000 13.5 for 19.1; a launch less on the host, 2.7).
+// Each keeps the contraction splits that its own launch would have, so the bits do not depend on what else is
+// asked for, and a cluster of the larger split may hold several tiles of the other product.
+struct BothPlan {
+  int bx, bw, cluster;  // bx 0: separate launches
+  int nx, nw;           // blocks of each, whole clusters
+};
+static BothPlan plan_both(int64_t M, int64_t N, int64_t K, const Plan& px, const Plan& pw) {
+  const int sx = px.pair ? 1 : px.splits, sw = pw.pair ? 1 : pw.splits, c = std::max(sx, sw), sms = num_sms();
+  const int64_t tp = (K + BP - 1) / BP;
+  BothPlan best{};
+  double tb = px.us + pw.us;
+  for (int bx = 16; bx <= 128; bx *= 2)
+    for (int bw = 64; bw <= 128; bw *= 2) {
+      const int64_t nx = (tp * ((M + bx - 1) / bx) * sx + c - 1) / c * c;
+      const int64_t nw = (tp * ((N + bw - 1) / bw) * sw + c - 1) / c * c;
+      if ((double)(nx + nw) > split_fit(c, sms)) continue;
+      const double t = std::max(split_us(bx, kblocks(N), sx), split_us(bw, kblocks(M), sw));
+      if (t < tb) tb = t, best = BothPlan{bx, bw, c, (int)nx, (int)nw};
+    }
+  return best;
+}
+template <int BX, int BW>
+static lsq_status launch_both(const Both& b, const BothPlan& plan, cudaStream_t stream) {
+  static int configured[64] = {0};
+  constexpr int bytes = Cfg<BX>::BYTES > Cfg<BW>::BYTES ? Cfg<BX>::BYTES : Cfg<BW>::BYTES;
+  int dev = 0;
+  LSQ_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev >= 0 && dev < 64 && !configured[dev]) {
+    LSQ_CUDA_TRY(cudaFuncSetAttribute(linear_both_kernel<BX, BW>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    configured[dev] = 1;
+  }
+  return launch_chained("linear_both_kernel", linear_both_kernel<BX, BW>, dim3((unsigned)(plan.nx + plan.nw)), NTHREADS,
+                        bytes, (unsigned)plan.cluster, stream, b);
+}
+static lsq_status both(const BothPlan& plan, const Plan& px, const Plan& pw, const void* dz, const void* x,
+                       const void* w, int64_t M, int64_t N, int64_t K, const Epi& ex, const Epi& ew,
+                       cudaStream_t stream) {
+  Both b;
+  b.nx = plan.nx;
+  lsq_status st = split_args(&b.mx, &b.x, w, 1, dz, 0, K, M, N, plan.bx, px.pair ? 1 : px.splits, ex);
+  if (st == LSQ_OK) st = split_args(&b.mw, &b.w, x, 1, dz, 1, K, N, M, plan.bw, pw.pair ? 1 : pw.splits, ew);
+  if (st != LSQ_OK) return st;
+  if (plan.bw == 64) {
+    if (plan.bx == 16) return launch_both<16, 64>(b, plan, stream);
+    if (plan.bx == 32) return launch_both<32, 64>(b, plan, stream);
+    if (plan.bx == 64) return launch_both<64, 64>(b, plan, stream);
+    return launch_both<128, 64>(b, plan, stream);
+  }
+  if (plan.bx == 16) return launch_both<16, 128>(b, plan, stream);
+  if (plan.bx == 32) return launch_both<32, 128>(b, plan, stream);
+  if (plan.bx == 64) return launch_both<64, 128>(b, plan, stream);
+  return launch_both<128, 128>(b, plan, stream);
 }
 
 // ---------------------------------------------------------------- dz and db
@@ -927,7 +1020,7 @@ extern "C" lsq_status lsq_linear_fwd(const void* x, const void* w, const void* b
     return launch_chained("linear_row_kernel", lin::linear_row_kernel, dim3((unsigned)(N / 8)), 256, 0, 1,
                           (cudaStream_t)stream, p);
   }
-  return lin::product<0, 0>(w, x, N, M, K, e, (cudaStream_t)stream);
+  return lin::product<0, 0>(lin::plan_product(N, M, lin::kblocks(K), 0, 0), w, x, N, M, K, e, (cudaStream_t)stream);
 }
 
 extern "C" size_t lsq_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act) {
@@ -985,17 +1078,17 @@ extern "C" lsq_status lsq_linear_bwd(const void* dy, const void* x, const void* 
     if (dbias && !cs && (st = nrm::col_sum(part, sp.n, N, N, N, dbias, nullptr, accumulate ? 1 : 0, s)) != LSQ_OK)
       return st;
   }
-  if (dx) {
-    lin::Epi e{};
-    e.out = dx;
-    if ((st = lin::product<1, 0>(w, dz, K, M, N, e, s)) != LSQ_OK) return st;
+  lin::Epi ex{}, ew{};
+  ex.out = dx;
+  ew.out = dw;
+  ew.f32 = dw_f32 ? 1 : 0;
+  ew.accumulate = accumulate ? 1 : 0;
+  const lin::Plan px = dx ? lin::plan_product(K, M, lin::kblocks(N), 1, 0) : lin::Plan{};
+  const lin::Plan pw = dw ? lin::plan_product(K, N, lin::kblocks(M), 1, 1) : lin::Plan{};
+  if (dx && dw) {
+    const lin::BothPlan plan = lin::plan_both(M, N, K, px, pw);
+    if (plan.bx) return lin::both(plan, px, pw, dz, x, w, M, N, K, ex, ew, s);
   }
-  if (dw) {
-    lin::Epi e{};
-    e.out = dw;
-    e.f32 = dw_f32 ? 1 : 0;
-    e.accumulate = accumulate ? 1 : 0;
-    if ((st = lin::product<1, 1>(x, dz, K, N, M, e, s)) != LSQ_OK) return st;
-  }
-  return LSQ_OK;
+  if (dx && (st = lin::product<1, 0>(px, w, dz, K, M, N, ex, s)) != LSQ_OK) return st;
+  return dw ? lin::product<1, 1>(pw, x, dz, K, N, M, ew, s) : LSQ_OK;
 }

@@ -700,8 +700,8 @@ def lsq_linear_bwd(dy, x, w, z, act: int, dx, dw, dw_f32: int, dbias, accumulate
     """dx, dw and dbias (each may be None) of lsq_linear_fwd from dy and the kept pre-activation z."""
     f, mn, bf, f32 = "lsq_linear_bwd", M * N, torch.bfloat16, torch.float32
     dev, st = _here(stream)
-    # at least: a tall dz pass adds a kernel for dbias
-    launches = (1 if act != ACT_NONE or dbias is not None else 0) + (dx is not None) + (dw is not None)
+    # at least: a tall dz pass adds a kernel for dbias, and a large dx and dw take one each
+    launches = (1 if act != ACT_NONE or dbias is not None else 0) + (dx is not None or dw is not None)
     _call(f, _t(f, "dy", dy, bf, mn, dev), _t(f, "x", x, bf, M * K, dev), _t(f, "w", w, bf, N * K, dev),
           _t(f, "z", z, bf, mn, dev), act, _t(f, "dx", dx, bf, M * K, dev),
           _t(f, "dw", dw, f32 if dw_f32 else bf, N * K, dev), dw_f32, _t(f, "dbias", dbias, f32, N, dev), accumulate,

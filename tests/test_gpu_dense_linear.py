@@ -241,3 +241,32 @@ def test_after_copies_and_joins_in_a_graph(lsq):
         assert (y20.double() - 2 * ref).norm() <= 2 ** -8 * (2 * ref).norm()
         ref = y0.double().t() @ s.double()
         assert (dw0.double() - ref).norm() <= 2e-5 * ref.norm()
+
+
+# both products in one launch: every pair of tile widths, equal and unequal splits, clusters that tiles do not fill
+# (148 SMs); the last three take separate launches
+TOGETHER = [(1, 8, 8), (194, 8, 8), (65, 264, 8), (1, 520, 8), (25, 384, 2480), (17, 328, 2640), (70, 536, 784),
+            (1, 456, 1056), (66, 8, 2936), (281, 72, 264), (187, 776, 8), (196, 536, 8), (475, 264, 264),
+            (1043, 1488, 8), (501, 2864, 8), (1670, 8, 136), (162, 8, 2400), (490, 2200, 8), (258, 784, 8),
+            (129, 136, 2080), (521, 72, 552), (971, 2056, 8), (289, 1296, 8), (314, 72, 2416), (430, 672, 864),
+            (2091, 400, 8), (449, 1560, 312), (278, 72, 2840), (585, 80, 848), (72, 792, 1152), (652, 2312, 8),
+            (479, 1920, 8), (8, 576, 1536), (33, 4096, 1024), (2048, 576, 1536)]
+
+
+@pytest.mark.parametrize("M,N,K", TOGETHER)
+def test_both_gradients_together_and_alone(lsq, M, N, K):
+    """dx and dW of one call: within the bounds, and bit for bit what each alone gives, in both output types."""
+    act = ACTS.index("silu")
+    t = _inputs(M, N, K, 11)
+    ws = torch.empty(lsq.lsq_linear_bwd_workspace_size(M, N, K, act), dtype=torch.uint8, device="cuda")
+    for f32 in (0, 1):
+        dx, dx1 = (torch.empty(M, K, dtype=BF, device="cuda") for _ in range(2))
+        dw, dw1 = (torch.full((N, K), 0.25, dtype=F32 if f32 else BF, device="cuda") for _ in range(2))
+        lsq.lsq_linear_bwd(t["dy"], t["x"], t["w"], t["z"], act, dx, dw, f32, None, f32, M, N, K, ws)
+        lsq.lsq_linear_bwd(t["dy"], None, t["w"], t["z"], act, dx1, None, 0, None, 0, M, N, K, ws)
+        lsq.lsq_linear_bwd(t["dy"], t["x"], None, t["z"], act, None, dw1, f32, None, f32, M, N, K, ws)
+        assert torch.equal(dx, dx1) and torch.equal(dw, dw1)
+        if not f32:
+            want = BB.linear_bwd(_d(t["dy"]), _d(t["x"]), _d(t["w"]), _d(t["z"]), "silu", M + 32, dw_f32=False)
+            _check(dx, want["dx"], "dx together", rel=8e-3)
+            _check(dw, want["dw"], "dw together", rel=8e-3)

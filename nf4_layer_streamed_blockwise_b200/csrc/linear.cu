@@ -169,32 +169,54 @@ struct Maps {
   CUtensorMap p, q;
 };
 
-// eight neighbouring columns of one output row: bias, z, activation, residual, one rounding, one store
-__device__ __forceinline__ void finish8(float (&v)[8], const Epi& e, int64_t off, int col) {
-  if (e.f32) {
+// What the epilogue of eight neighbouring columns of one output row reads, fetched ahead: the forward's residual, or
+// what an accumulating fp32 output holds.
+struct Ahead {
+  uint4 a, b;
+};
+template <bool FWD>
+__device__ __forceinline__ Ahead epi_fetch(const Epi& e, int64_t off, bool in) {
+  Ahead h{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (FWD && in && e.residual) h.a = *reinterpret_cast<const uint4*>(e.residual + off);
+  if (!FWD && in && e.accumulate) {
+    const uint4* o = reinterpret_cast<const uint4*>(static_cast<const float*>(e.out) + off);
+    h.a = o[0];
+    h.b = o[1];
+  }
+  return h;
+}
+__device__ __forceinline__ uint4 epi_bias(const Epi& e, int col, bool in) {
+  return in && e.bias ? *reinterpret_cast<const uint4*>(e.bias + col) : make_uint4(0u, 0u, 0u, 0u);
+}
+// forward: bias, z, activation, residual, one rounding, one store; a gradient: bf16, or fp32 (added)
+template <bool FWD>
+__device__ __forceinline__ void finish8(float (&v)[8], const Epi& e, int64_t off, uint4 bias, const Ahead& h) {
+  if (!FWD && e.f32) {
     float4* o = reinterpret_cast<float4*>(static_cast<float*>(e.out) + off);
     if (e.accumulate) {
-      const float4 a = o[0], b = o[1];
-      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      v[0] += __uint_as_float(h.a.x); v[1] += __uint_as_float(h.a.y);
+      v[2] += __uint_as_float(h.a.z); v[3] += __uint_as_float(h.a.w);
+      v[4] += __uint_as_float(h.b.x); v[5] += __uint_as_float(h.b.y);
+      v[6] += __uint_as_float(h.b.z); v[7] += __uint_as_float(h.b.w);
     }
     o[0] = make_float4(v[0], v[1], v[2], v[3]);
     o[1] = make_float4(v[4], v[5], v[6], v[7]);
     return;
   }
-  if (e.bias) {
+  if (FWD) {
     float b[8];
-    unpack8(*reinterpret_cast<const uint4*>(e.bias + col), b);
+    if (e.bias) {
+      unpack8(bias, b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
-  if (e.z) *reinterpret_cast<uint4*>(e.z + off) = pack8(v);
-  act_of(e.act, v);
-  if (e.residual) {
-    float r[8];
-    unpack8(*reinterpret_cast<const uint4*>(e.residual + off), r);
+      for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
+    if (e.z) *reinterpret_cast<uint4*>(e.z + off) = pack8(v);
+    act_of(e.act, v);
+    if (e.residual) {
+      unpack8(h.a, b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += r[i];
+      for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
   }
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(e.out) + off) = pack8(v);
 }
@@ -317,8 +339,19 @@ __device__ __forceinline__ void split_tile(const Maps& maps, const Params& p, in
     if (elect_one()) tc_commit(afull);  // also when a wait gave up: the epilogue is not left waiting
     __syncwarp();
   }
-  if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const int lper = p.lper, per = 1 << lper;  // output rows this CTA finishes
+  // a thread finishes eight columns (always the same) of the rows fr, fr + 16, ...; what it reads for them is under
+  // way before the sums are there (16 x 4096 x 4096 with bias and residual 9.1 us, now 7.9; an accumulating fp32 dW of
+  // 333 x 1536 x 576 with its dx 9.0, 7.4)
+  const int fr = (int)threadIdx.x / (BP / 8), fc = (int)threadIdx.x % (BP / 8) * 8;
+  const bool in = p0 + fc < p.P;
+  const int64_t off0 = (int64_t)(q0 + rank * per) * p.P + p0 + fc;
+  auto fetch = [&](int r) {
+    return epi_fetch<!PMN>(p.e, off0 + (int64_t)r * p.P, in && r < per && q0 + rank * per + r < p.Q);
+  };
+  const uint4 bias = epi_bias(p.e, p0 + fc, in && !PMN);
+  Ahead ahead = fetch(fr);
+  if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (warp < 4) {
     const bool ok = __all_sync(0xffffffffu, mbar_wait(afull, 0, 731));
     tc_fence_after();
@@ -354,22 +387,22 @@ __device__ __forceinline__ void split_tile(const Maps& maps, const Params& p, in
     tmem_dealloc(tmem, C::TCOLS);
   }
   const float* xs = reinterpret_cast<const float*>(smem + C::OFF_X);
-#pragma unroll 1
-  for (int it = threadIdx.x; it < per * (BP / 8); it += NTHREADS) {
-    const int r = it / (BP / 8), c = (it % (BP / 8)) * 8;
-    const int q = q0 + rank * per + r, col = p0 + c;
-    if (q >= p.Q || col >= p.P) continue;
+  if (!in) return;
+#pragma unroll 2  // 512 x 2048 x 2048: 10.2 us rolled, 9.9 by two, 9.9 by four
+  for (int r = fr; r < per && q0 + rank * per + r < p.Q; r += NTHREADS / (BP / 8)) {
+    const Ahead h = ahead;
+    ahead = fetch(r + NTHREADS / (BP / 8));
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
 #pragma unroll 1
     for (int k = 0; k < S; ++k) {  // rank order
-      const float4* a = reinterpret_cast<const float4*>(xs + ((k << lper) + r) * BP + c);
+      const float4* a = reinterpret_cast<const float4*>(xs + ((k << lper) + r) * BP + fc);
       const float4 lo = a[0], hi = a[1];
       v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
       v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
     }
-    finish8(v, p.e, (int64_t)q * p.P + col, col);
+    finish8<!PMN>(v, p.e, off0 + (int64_t)r * p.P, bias, h);
   }
 }
 
@@ -545,18 +578,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GTHREADS, 1)
       const int row0 = (t % ntm) * TM + (int)rank * 128 + (warp & 3) * 32, n0 = (t / ntm) * p.bn;
       const int buf = j & 1, row = row0 + lane;
       const int nc = row0 < p.Q ? (min(p.bn, p.P - n0) + 31) / 32 : 0;  // 32-column pieces inside the output
+      // under way before the products are done: the bias of the warp's four pieces, sixteen bytes a lane, and each
+      // piece's residual while the piece before it is finished (read where they are used they cost each piece
+      // their latency: 8192 x 2048 x 128 with bias 19.3 us, not 13.5, 2048 x 4096 x 1024 24.2, not 19.7)
+      uint4 bw = make_uint4(0u, 0u, 0u, 0u), rv[4];
+      const int bcol = n0 + (wg + (lane >> 2) * 2) * 32 + (lane & 3) * 8;
+      if (!F32 && e.bias && lane < 16 && bcol < p.P) bw = *reinterpret_cast<const uint4*>(e.bias + bcol);
+      auto fetch_residual = [&](int c) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = n0 + c * 32 + q * 8;
+          rv[q] = (c < nc && row < p.Q && col < p.P)
+                      ? *reinterpret_cast<const uint4*>(e.residual + (int64_t)row * p.P + col)
+                      : make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      if (!F32 && e.residual) fetch_residual(wg);
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u, 741))) break;
       tc_fence_after();
       for (int c = wg; c < nc; c += 2) {
         const int col = n0 + c * 32;
-        uint4 rv[4];
-        if (!F32 && e.residual) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            rv[q] = (row < p.Q && col + q * 8 < p.P)
-                        ? *reinterpret_cast<const uint4*>(e.residual + (int64_t)row * p.P + col + q * 8)
-                        : make_uint4(0u, 0u, 0u, 0u);
-        }
         float v[32];
         tmem_ld32(tmem + lane_base + (uint32_t)(buf * 256 + c * 32), v);
         tc_wait_ld_regs(v);
@@ -581,9 +622,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GTHREADS, 1)
         if (e.bias) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            if (col + q * 8 >= p.P) break;
+            const int from = (c >> 1) * 4 + q;
             float b[8];
-            unpack8(*reinterpret_cast<const uint4*>(e.bias + col + q * 8), b);
+            unpack8(make_uint4(__shfl_sync(0xffffffffu, bw.x, from), __shfl_sync(0xffffffffu, bw.y, from),
+                               __shfl_sync(0xffffffffu, bw.z, from), __shfl_sync(0xffffffffu, bw.w, from)), b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[q * 8 + i] += b[i];
           }
@@ -609,6 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GTHREADS, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[q * 8 + i] += r[i];
           }
+          fetch_residual(c + 2);
         }
         if (lane == 0) bulk_wait_read<1>();
         __syncwarp();
@@ -658,7 +701,8 @@ static lsq_status launch_pair(const GMaps& maps, const Params& p, int64_t tiles,
 // A generated token: the weight is read once and HBM decides, so no tensor core and no tile: a block takes
 // eight output columns, its warps share the contraction (warp w the 256-wide steps w, w + 8, ...), a lane
 // multiplies 16-byte words of the eight weight rows with the row's words of x in f32x2, and the warps' sums
-// join in shared memory in warp order.  Eight 16-byte loads a lane and step are in flight.  Weights from HBM,
+// join in shared memory in warp order.  Eight 16-byte loads a lane and step are in flight, and four blocks run on
+// an SM (4096 x 4096 7.4 us with three, 6.4 with four, over three weights that L2 holds in part).  Weights from HBM,
 // graph replays, against the tiles above: 4096 x 4096 8.0 us (8.9), 14336 x 4096 21.7 (22.6), 576 x 1536 2.4
 // (3.8); the same kernel with two rows loses from 1 M weights on (13.5 us for 9.0: its products take over).
 struct OneRow {
@@ -666,7 +710,7 @@ struct OneRow {
   int N, k8;  // output columns, words of a row
   Epi e;
 };
-__global__ void __launch_bounds__(256) linear_row_kernel(const __grid_constant__ OneRow p) {
+__global__ void __launch_bounds__(256, 4) linear_row_kernel(const __grid_constant__ OneRow p) {
   __shared__ float part[8][8];
   grid_release();
   grid_wait();
@@ -690,6 +734,8 @@ __global__ void __launch_bounds__(256) linear_row_kernel(const __grid_constant__
       for (int j = 0; j < 4; ++j) acc[f] = fma2(xv[j], u[j], acc[f]);
     }
   }
+  const uint4 bias = epi_bias(p.e, col, threadIdx.x == 0);
+  const Ahead ahead = epi_fetch<true>(p.e, col, threadIdx.x == 0);
 #pragma unroll
   for (int f = 0; f < 8; ++f) {
     const float v = nrm::warp_sum(nrm::pair_sum(acc[f]));
@@ -704,7 +750,7 @@ __global__ void __launch_bounds__(256) linear_row_kernel(const __grid_constant__
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[f] += part[k][f];
   }
-  finish8(v, p.e, col, col);
+  finish8<true>(v, p.e, col, bias, ahead);
 }
 
 // K-major operand [rows, C] with box {64, brows}; MN-major operand [C, rows] with box {64, 64}

@@ -1006,15 +1006,16 @@ __global__ void __launch_bounds__(256, 4) dz_kernel(const uint4* __restrict__ dy
 }
 
 // row strips of dz_kernel: one round of its blocks (four per SM), at least 8 rows each; at most eight, joined in a
-// cluster, where they fill that round or leave no more than 4 rows a warp (2048 x 14336, 448 of 592 blocks: 43 us
-// joined, 38 with ten strips and a second kernel)
+// cluster, where they fill that round or a warp's rows take no longer than the second kernel: 4 with an activation
+// (M = 333, N = 1536, GELU: 5.0 us joined, 5.1 in two kernels; 512 x 1024 6.0 and 4.4; 2048 x 14336, 448 of 592
+// blocks, 43 and 38), 16 without (512 x 1024 2.8 and 3.6, 1024 x 4096 4.2 and 4.5); the host saves 2.3 us
 struct Strips {
   int64_t rows;
   int n, joined;
 };
-static Strips strips_of(int64_t M, int64_t N) {
+static Strips strips_of(int64_t M, int64_t N, int act) {
   const int64_t cb = (N + 255) / 256, slots = 4 * num_sms();
-  const bool join = 8 * cb >= slots || M <= 256;
+  const bool join = 8 * cb >= slots || M <= (act == LSQ_ACT_NONE ? 1024 : 256);
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(slots / cb, join ? 8 : slots));
   Strips s;
   s.rows = std::max<int64_t>(8, (M + want - 1) / want);
@@ -1072,7 +1073,7 @@ extern "C" lsq_status lsq_linear_fwd(const void* x, const void* w, const void* b
 extern "C" size_t lsq_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act) {
   if (M < 1 || N < 8 || K < 8) return 256;
   return (act == LSQ_ACT_NONE ? 0 : lin::round256((size_t)M * (size_t)N * 2)) +
-         lin::round256((size_t)lin::strips_of(M, N).n * (size_t)N * sizeof(float));
+         lin::round256((size_t)lin::strips_of(M, N, act).n * (size_t)N * sizeof(float));
 }
 
 extern "C" lsq_status lsq_linear_bwd(const void* dy, const void* x, const void* w, const void* z, int32_t act, void* dx,
@@ -1109,7 +1110,7 @@ extern "C" lsq_status lsq_linear_bwd(const void* dy, const void* x, const void* 
       ws += lin::round256((size_t)M * (size_t)N * 2);
     }
     float* part = reinterpret_cast<float*>(ws);
-    const lin::Strips sp = lin::strips_of(M, N);
+    const lin::Strips sp = lin::strips_of(M, N, act);
     const int64_t blocks = (N + 255) / 256 * sp.n;
     const int n8 = (int)(N / 8), cs = sp.joined ? sp.n : 0;
     auto k = act == LSQ_ACT_RELU        ? lin::dz_kernel<LSQ_ACT_RELU>

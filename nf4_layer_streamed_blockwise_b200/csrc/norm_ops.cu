@@ -275,7 +275,7 @@ struct Bwd {
   const uint4* res;   // dres_in or null; may alias out
   uint4* out;
   float* part;        // [gridDim.x][2][d]: the blocks' sums of dy xhat and dy (GRADS)
-  float *dg, *db;     // written here when the grid is one block or one cluster
+  float *dg, *db;     // few rows: written in the one kernel
   int64_t rows;
   int d8, nb, accumulate;
   float inv_d;
@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) rms_bwd_unpa
 
 // LayerNorm: out = res + rs (a - mean(a) - xh mean(a xh)), a = dy g, xh = (x - mean) rs.  Warps (d <= 768)
 // or blocks walk the rows in strides and a thread's columns stay the same, so the sums over rows of dy xh
-// and dy (dg, db) collect in registers and leave once per block; col_sum_kernel adds the blocks in order.
-// The arithmetic runs on pairs (f32x2): scalar, its 30 operations an element took as long as the loads.
+// and dy (dg, db) collect in registers and leave once per block; col_sum_kernel adds the blocks in order.  Few rows
+// have a kernel of their own.  The arithmetic runs on pairs (f32x2): scalar, its 30 operations an element took as long as the loads.
 
 // one word of the first pass: xh and a, their row sums, and the column sums of dy xh and dy
 template <bool GRADS>
@@ -369,41 +369,11 @@ __device__ __forceinline__ uint4 ln_bwd_out(const uint64_t (&xh)[4], const uint6
   for (int j = 0; j < 4; ++j) o[j] = fma2(xh[j], nk2, add2(fma2(a[j], rs, o[j]), nk1));
   return pack_pairs(o);
 }
-// eight column sums of word c, to row r of the partial sums or (last) to dg / db
-__device__ __forceinline__ void ln_put_sums(const Bwd& p, int r, bool last, int h, int c, const float (&v)[8]) {
-  const int d = p.d8 * 8;
-  float* o = last ? (h ? p.db : p.dg) : p.part + ((int64_t)r * 2 + h) * d;
-  if (!o) return;
-  float4* o4 = reinterpret_cast<float4*>(o + c * 8);
-  float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
-  if (last && p.accumulate) {
-    const float4 x = o4[0], y = o4[1];
-    lo.x += x.x; lo.y += x.y; lo.z += x.z; lo.w += x.w;
-    hi.x += y.x; hi.y += y.y; hi.z += y.z; hi.w += y.w;
-  }
-  o4[0] = lo;
-  o4[1] = hi;
-}
-// Few rows: the blocks are one cluster, each leaves its sums in shared memory (xs: [h][d / 4]), and each finishes
-// its share of the words from all of them, in rank order: no second kernel (a launch costs the host 2.4 us).
-constexpr int MAX_CS = 8;
-__device__ __forceinline__ void ln_join_sums(const Bwd& p, const float4* xs, int cs) {
-  nf4g::cluster_sync_all();
-  const int d8 = p.d8, n = (int)blockDim.x;
-  for (int it = (int)nf4g::cluster_ctarank() * n + (int)threadIdx.x; it < 2 * d8; it += cs * n) {
-    const int h = it >= d8, c = it - h * d8;
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    for (int k = 0; k < cs; ++k) {
-      const uint32_t a = nf4g::cluster_addr(xs + it * 2, (uint32_t)k);
-      const float4 lo = nf4g::ldn::ld_dsmem_f4(a), hi = nf4g::ldn::ld_dsmem_f4(a + 16);
-      v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-      v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
-    }
-    ln_put_sums(p, 0, true, h, c, v);
-  }
-  nf4g::cluster_sync_all();  // the sums stay until every block has read its share
+// eight column sums of word c, to row r of the partial sums
+__device__ __forceinline__ void ln_put_sums(const Bwd& p, int r, int h, int c, const float (&v)[8]) {
+  float4* o = reinterpret_cast<float4*>(p.part + ((int64_t)r * 2 + h) * (p.d8 * 8) + c * 8);
+  o[0] = make_float4(v[0], v[1], v[2], v[3]);
+  o[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 __device__ __forceinline__ void split8(const uint64_t* s, float (&v)[8]) {
 #pragma unroll
@@ -427,11 +397,10 @@ __device__ __forceinline__ void ln_fetch(const Bwd& p, uint8_t* b, uint64_t* bar
 // a row per warp, V words a lane
 constexpr int LNW = 8;
 template <int V, bool GRADS>
-__global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_constant__ Bwd p, int nst, int stage, int cs) {
+__global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_constant__ Bwd p, int nst, int stage) {
   extern __shared__ __align__(128) uint8_t smem[];  // per warp [nst][x | dy | res], then every stage's barrier
   __shared__ float comb[LNW * 32 * 9];
   __shared__ int gave_up[LNW];  // stage and parity of a wait that did (in registers it costs the loop 1%)
-  __shared__ float4 xs[GRADS ? 2 * V * 64 : 1];  // this block's sums, for ln_join_sums
   const int t = (int)(threadIdx.x & 31), w = (int)(threadIdx.x >> 5);
   uint8_t* ring = smem + (size_t)w * nst * stage;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)LNW * nst * stage) + w * nst;
@@ -504,15 +473,9 @@ __global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_c
         for (int k = 1; k < LNW; ++k)
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] += comb[(k * 32 + t) * 9 + j];
-        if (cs == 1) {
-          ln_put_sums(p, (int)blockIdx.x, gridDim.x == 1, h, c, v);
-        } else {
-          xs[(h * d8 + c) * 2] = make_float4(v[0], v[1], v[2], v[3]);
-          xs[(h * d8 + c) * 2 + 1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
+        ln_put_sums(p, (int)blockIdx.x, h, c, v);
       }
     }
-    if (cs > 1) ln_join_sums(p, xs, cs);
   }
 }
 
@@ -520,7 +483,7 @@ __global__ void __launch_bounds__(LNW * 32, 2) ln_bwd_warp_kernel(const __grid_c
 // every thread is then done with it.
 template <int V, bool GRADS>
 __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
-    ln_bwd_block_kernel(const __grid_constant__ Bwd p, int nst, int stage, int cs) {
+    ln_bwd_block_kernel(const __grid_constant__ Bwd p, int nst, int stage) {
   extern __shared__ __align__(128) uint8_t ring[];  // [nst][x | dy | res], then the stages' barriers
   __shared__ float2 red[2][16];
   __shared__ int gave_up;
@@ -592,8 +555,6 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
   }
   if (!ok && t == 0) mbar_drain(full, nst, gave_up >> 1, (uint32_t)gave_up & 1u, 462);
   if constexpr (GRADS) {
-    float4* xs = reinterpret_cast<float4*>(ring);  // in place of the ring
-    if (cs > 1) __syncthreads();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = t + i * T;
@@ -602,15 +563,107 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 320, V == 4 ? 1 : 2)
       for (int h = 0; h < 2; ++h) {
         float v[8];
         split8(h ? sb[i] : sg[i], v);
-        if (cs == 1) {
-          ln_put_sums(p, (int)blockIdx.x, gridDim.x == 1, h, c, v);
-        } else {
-          xs[(h * d8 + c) * 2] = make_float4(v[0], v[1], v[2], v[3]);
-          xs[(h * d8 + c) * 2 + 1] = make_float4(v[4], v[5], v[6], v[7]);
+        ln_put_sums(p, (int)blockIdx.x, h, c, v);
+      }
+    }
+  }
+}
+
+// Few rows: the statistics are inputs, so the column sums need no row reduction, and a second reading of x and dy
+// (from L2) costs less than partial sums and their kernel.  One launch: the first col_blocks blocks add 8 << seg
+// columns each over all rows (1 << seg lanes hold a row's words of them; the groups' sums join by shuffles, then
+// the warps' in shared memory, in order), the others take a row each, or (WARP) eight.  Wide column blocks for the
+// fewest rows: 10 x 16384 3.1 us, not 6.6 with 32 columns in each.
+constexpr int FEW_PITCH = 17;  // sixteen sums a word, apart in the banks
+template <int V, bool WARP>
+__global__ void __launch_bounds__(512) ln_bwd_few_kernel(const __grid_constant__ Bwd p, int col_blocks, int seg) {
+  extern __shared__ float comb[];  // [warps][1 << seg][FEW_PITCH]
+  __shared__ float2 red[16];
+  grid_release();
+  grid_wait();
+  const int w = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, nw = (int)blockDim.x >> 5, d8 = p.d8;
+  if ((int)blockIdx.x < col_blocks) {
+    const int wide = 1 << seg, at = lane & (wide - 1), step = nw << (5 - seg);
+    const int64_t c = ((int64_t)blockIdx.x << seg) + at;
+    uint64_t sg[4] = {0ull, 0ull, 0ull, 0ull}, sb[4] = {0ull, 0ull, 0ull, 0ull};
+    if (c < d8) {
+#pragma unroll 4
+      for (int64_t r = (int)threadIdx.x >> seg; r < p.rows; r += step) {
+        uint64_t x[4], d[4];
+        const float mu = p.mean[r], rs = p.rstd[r];
+        unpack_pairs(p.x[r * d8 + c], x);
+        unpack_pairs(p.dy[r * d8 + c], d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sg[j] = fma2(d[j], mul2(add2(x[j], f2(-mu, -mu)), f2(rs, rs)), sg[j]);
+          sb[j] = add2(sb[j], d[j]);
         }
       }
     }
-    if (cs > 1) ln_join_sums(p, xs, cs);
+    float* mine = comb + ((w << seg) + at) * FEW_PITCH;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 v = f2split(j < 4 ? sg[j & 3] : sb[j & 3]);
+      float a = v.x, b = v.y;
+      for (int o = wide; o < 32; o <<= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+      }
+      if (lane < wide) {
+        mine[2 * j] = a;
+        mine[2 * j + 1] = b;
+      }
+    }
+    __syncthreads();
+    for (int it = (int)threadIdx.x; it < 16 << seg; it += (int)blockDim.x) {  // a column's sum: dg's, then db's
+      const int h = it >> (seg + 3), k = it & ((8 << seg) - 1);
+      const int64_t col = ((int64_t)blockIdx.x << (seg + 3)) + k;
+      float* o = h ? p.db : p.dg;
+      if (!o || col >= (int64_t)d8 * 8) continue;
+      float v = 0.0f;
+      for (int i = 0; i < nw; ++i) v += comb[((i << seg) + (k >> 3)) * FEW_PITCH + h * 8 + (k & 7)];
+      o[col] = p.accumulate ? o[col] + v : v;
+    }
+    return;
+  }
+  const int T = WARP ? 32 : (int)blockDim.x, t = WARP ? lane : (int)threadIdx.x;
+  const int64_t blk = (int64_t)blockIdx.x - col_blocks, row = WARP ? blk * nw + w : blk;
+  if (WARP && row >= p.rows) return;  // whole warps; no block barrier follows
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  const int64_t base = row * d8;
+  uint4 xv[V], dv[V], gv[V], rv[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {  // padded words: dy = g = 0
+    const int c = t + i * T;
+    const bool in = c < d8;
+    xv[i] = in ? p.x[base + c] : z;
+    dv[i] = in ? p.dy[base + c] : z;
+    gv[i] = in ? p.g[c] : z;
+    rv[i] = in && p.res ? p.res[base + c] : z;
+  }
+  const float mu = p.mean[row], r = p.rstd[row];
+  const uint64_t nmu = f2(-mu, -mu), rs = f2(r, r);
+  uint64_t xh[4], a[4], s1 = 0ull, s2 = 0ull;
+#pragma unroll
+  for (int i = 0; i < V; ++i) ln_bwd_word<false>(xv[i], dv[i], gv[i], nmu, rs, xh, a, s1, s2, nullptr, nullptr);
+  float2 sum = make_float2(warp_sum(pair_sum(s1)), warp_sum(pair_sum(s2)));
+  if (!WARP) {
+    if (lane == 0) red[w] = sum;
+    __syncthreads();
+    sum = make_float2(0.0f, 0.0f);
+    for (int k = 0; k < nw; ++k) {
+      sum.x += red[k].x;
+      sum.y += red[k].y;
+    }
+  }
+  const float k1 = -r * sum.x * p.inv_d, k2 = -r * sum.y * p.inv_d;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = t + i * T;
+    if (c >= d8) break;
+    uint64_t u1 = 0ull, u2 = 0ull;
+    ln_bwd_word<false>(xv[i], dv[i], gv[i], nmu, rs, xh, a, u1, u2, nullptr, nullptr);
+    p.out[base + c] = ln_bwd_out(xh, a, rv[i], rs, f2(k1, k1), f2(k2, k2));
   }
 }
 
@@ -694,9 +747,13 @@ static Geo row_geo(int64_t rows, int d8, Pass pass) {
 // reductions (two blocks of 320 threads: 61 us for 8192 x 5120; one block of two such groups, which halves
 // the partial sums: 72) and share its registers and shared memory (rings of nst stages of `stage` bytes).
 struct BwdGeo {
-  int v, threads, warp, nst, stage, cluster;
+  int v, threads, warp, nst, stage;
   unsigned blocks;
 };
+// Rows for the one kernel of few rows, with dg and db against the rings and their second kernel: 333 x 576 3.1 us for
+// 6.6, 130 x 2048 3.3 for 5.4, 10 x 5120 2.0 for 5.6, 1000 x 5120 11.6 for 16.6, 1500 x 2048 9.9 for 12.7; but 1500 x
+// 64 7.3 for 5.5, 2000 x 576 8.2 for 7.1, 1000 x 9912 29.8 for 27.2.  The host saves 2.4 us.
+static bool few_rows(int64_t rows, int d8) { return rows <= (d8 < 64 ? 1024 : 1536) && rows * d8 <= 1 << 20; }
 constexpr int RING_BYTES = 200 * 1024;
 static BwdGeo ln_bwd_geo(int64_t rows, int d8, bool grads) {
   BwdGeo g{};
@@ -712,16 +769,11 @@ static BwdGeo ln_bwd_geo(int64_t rows, int d8, bool grads) {
     g.threads = (((d8 + g.v - 1) / g.v) + 31) / 32 * 32;
     occ = g.v == 4 ? (g.threads <= 256 ? 2 : 1) : std::max(2, std::min(6, 640 / g.threads));
   }
-  // up to two rows a walker of one cluster: its blocks join their sums themselves (130 x 576 7.8 us in one launch,
-  // 5.7 in two, but the second costs the host 2.4; at 333 x 576 it would be 11.7 for 5.7)
-  const bool few = grads && rows <= 2 * (int64_t)per * MAX_CS;
   // each block's sums are 8 d bytes to write and to add: whole rounds of blocks with about four rows each pay for
   // them (1000 x 2048: 9.5 / 8.3 / 9.0 / 10.8 / 12.4 us with 1 to 5 blocks per SM; 10.2 with 250 blocks)
-  if (grads && !few && !g.warp) occ = (int)std::min<int64_t>(occ, (rows + 4 * num_sms() - 1) / (4 * num_sms()));
+  if (grads && !g.warp) occ = (int)std::min<int64_t>(occ, (rows + 4 * num_sms() - 1) / (4 * num_sms()));
   g.nst = std::max(2, std::min(8, RING_BYTES / occ / per / g.stage));
-  const int64_t most = few ? MAX_CS : (int64_t)occ * num_sms();
-  g.blocks = (unsigned)std::min((rows + per - 1) / per, most);
-  g.cluster = few ? (int)g.blocks : 1;
+  g.blocks = (unsigned)std::min<int64_t>((rows + per - 1) / per, (int64_t)occ * num_sms());
   return g;
 }
 
@@ -757,17 +809,42 @@ static lsq_status run_ln_bwd(const Bwd& p, const BwdGeo& g, cudaStream_t s) {
     lsq_status st = ring_smem(ln_bwd_warp_kernel<V, GRADS>, configured);
     if (st != LSQ_OK) return st;
     return launch_chained("ln_bwd_warp_kernel", ln_bwd_warp_kernel<V, GRADS>, dim3(g.blocks), (unsigned)g.threads, smem,
-                          (unsigned)g.cluster, s, p, g.nst, g.stage, g.cluster);
+                          1, s, p, g.nst, g.stage);
   } else {
     lsq_status st = ring_smem(ln_bwd_block_kernel<V, GRADS>, configured);
     if (st != LSQ_OK) return st;
     return launch_chained("ln_bwd_block_kernel", ln_bwd_block_kernel<V, GRADS>, dim3(g.blocks), (unsigned)g.threads,
-                          smem, (unsigned)g.cluster, s, p, g.nst, g.stage, g.cluster);
+                          smem, 1, s, p, g.nst, g.stage);
   }
 }
 template <int V, bool WARP>
 static lsq_status run_ln_bwd(const Bwd& p, bool grads, const BwdGeo& g, cudaStream_t s) {
   return grads ? run_ln_bwd<V, WARP, true>(p, g, s) : run_ln_bwd<V, WARP, false>(p, g, s);
+}
+
+static lsq_status run_ln_bwd_few(const Bwd& p, bool grads, cudaStream_t s) {
+  const int d8 = p.d8;
+  const bool warp = d8 <= 128;
+  const unsigned threads = d8 > 1024 ? 512 : 256;
+  auto k = warp ? (d8 <= 32   ? ln_bwd_few_kernel<1, true>
+                   : d8 <= 64 ? ln_bwd_few_kernel<2, true>
+                              : ln_bwd_few_kernel<4, true>)
+                : (d8 <= 256   ? ln_bwd_few_kernel<1, false>
+                   : d8 <= 512 ? ln_bwd_few_kernel<2, false>
+                               : ln_bwd_few_kernel<4, false>);
+  // the widest column blocks that leave a thread no more than two rows, at least 32 columns (64 bytes of a row)
+  int seg = 5;
+  while (seg > 2 && p.rows > 2 * (int64_t)(threads >> seg)) --seg;
+  const int cols = grads ? (d8 + (1 << seg) - 1) >> seg : 0;
+  const size_t smem = (size_t)(threads / 32) * FEW_PITCH * sizeof(float) << seg;
+  const unsigned rows = (unsigned)(warp ? (p.rows + 7) / 8 : p.rows);
+  const char* what = "ln_bwd_few_kernel";
+  // in place over dy or x the sums have to be read first
+  if (grads && (p.out == p.dy || p.out == p.x)) {
+    lsq_status st = launch_chained(what, k, dim3((unsigned)cols), threads, smem, 1, s, p, cols, seg);
+    return st != LSQ_OK ? st : launch_chained(what, k, dim3(rows), threads, 0, 1, s, p, 0, seg);
+  }
+  return launch_chained(what, k, dim3((unsigned)cols + rows), threads, smem, 1, s, p, cols, seg);
 }
 
 // the shape and alignment rules of the section, with this file's limits
@@ -835,6 +912,7 @@ extern "C" lsq_status lsq_layernorm_fwd(const void* x, const void* g, const void
 
 extern "C" size_t lsq_layernorm_bwd_workspace_size(int64_t rows, int64_t d) {
   if (rows < 1 || d < 8 || d > nrm::MAX_D) return 256;
+  if (nrm::few_rows(rows, (int)(d / 8))) return 256;
   const nrm::BwdGeo g = nrm::ln_bwd_geo(rows, (int)(d / 8), true);
   return ((size_t)g.blocks * 2 * (size_t)d * sizeof(float) + 255) / 256 * 256;
 }
@@ -878,8 +956,9 @@ extern "C" lsq_status lsq_layernorm_bwd(const void* dy, const void* x, const voi
   p.d8 = (int)(d / 8);
   p.accumulate = accumulate ? 1 : 0;
   p.inv_d = 1.0f / (float)d;
-  const nrm::BwdGeo ge = nrm::ln_bwd_geo(rows, p.d8, grads);
   cudaStream_t s = (cudaStream_t)stream;
+  if (nrm::few_rows(rows, p.d8)) return nrm::run_ln_bwd_few(p, grads, s);
+  const nrm::BwdGeo ge = nrm::ln_bwd_geo(rows, p.d8, grads);
   if (ge.warp)
     st = ge.v == 1   ? nrm::run_ln_bwd<1, true>(p, grads, ge, s)
          : ge.v == 2 ? nrm::run_ln_bwd<2, true>(p, grads, ge, s)
@@ -887,7 +966,7 @@ extern "C" lsq_status lsq_layernorm_bwd(const void* dy, const void* x, const voi
   else
     st = ge.v == 2 ? nrm::run_ln_bwd<2, false>(p, grads, ge, s) : nrm::run_ln_bwd<4, false>(p, grads, ge, s);
   if (st != LSQ_OK) return st;
-  if (!grads || ge.blocks == (unsigned)ge.cluster) return LSQ_OK;
+  if (!grads) return LSQ_OK;
   return nrm::col_sum(p.part, (int)ge.blocks, 2 * d, d, 2 * d, dg, db, p.accumulate, s);
 }
 

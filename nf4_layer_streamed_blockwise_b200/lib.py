@@ -623,8 +623,8 @@ def lsq_layernorm_bwd(dy, x, g, mean, rstd, dres_in, dres_out, dg, db, accumulat
     """dres_out = dres_in + dx; dg, db fp32 (None: frozen), overwritten or (accumulate=1) added to."""
     f, n, bf, f32 = "lsq_layernorm_bwd", rows * d, torch.bfloat16, torch.float32
     dev, st = _here(stream)
-    # few rows (one cluster's) need no second kernel
-    two = (dg is not None or db is not None) and rows > (128 if d <= 768 else 16)
+    # few rows need no second kernel
+    two = (dg is not None or db is not None) and (rows > (1024 if d < 512 else 1536) or rows * d > 1 << 23)
     _call(f, _t(f, "dy", dy, bf, n, dev), _t(f, "x", x, bf, n, dev), _t(f, "g", g, bf, d, dev),
           _t(f, "mean", mean, f32, rows, dev), _t(f, "rstd", rstd, f32, rows, dev),
           _t(f, "dres_in", dres_in, bf, n, dev), _t(f, "dres_out", dres_out, bf, n, dev), _t(f, "dg", dg, f32, d, dev),

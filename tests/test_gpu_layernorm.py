@@ -176,3 +176,38 @@ def test_in_place(lsq, rows, d):
 def test_forward_of_more_rows_than_run_at_once(lsq, rows, d, bias):
     """Two words a thread (the other widths are among the shapes above), and both sides of where it begins."""
     test_forward(lsq, rows, d, bias)
+
+
+# the walkers with their second kernel, by warps and by blocks of each width, and both sides of where they begin
+MANY = [(1025, 504), (1024, 504), (1100, 64), (1537, 512), (1536, 512), (1540, 264), (2000, 576), (1700, 768),
+        (1540, 1032), (2100, 2304), (1600, 5128), (1700, 4096), (600, 16384), (512, 16384), (513, 16384)]
+
+
+@pytest.mark.parametrize("rows,d", MANY)
+@pytest.mark.parametrize("res", [True, False])
+def test_backward_of_many_rows(lsq, rows, d, res):
+    test_backward(lsq, rows, d, res)
+
+
+@pytest.mark.parametrize("rows,d", [(2000, 520), (1540, 1160), (600, 16384), (1536, 512), (1024, 64), (1, 8), (33, 8200)])
+def test_in_place_at_other_sizes(lsq, rows, d):
+    test_in_place(lsq, rows, d)
+
+
+def test_few_rows_captured_in_place(lsq):
+    """In place over dy the sums are a launch of their own, before the rows': captured, replayed twice."""
+    rows, d = 200, 1000
+    t = _inputs(rows, d, seed=9)
+    mean, rstd = _stats(t["x"], 1e-5)
+    ws = torch.empty(lsq.lsq_layernorm_bwd_workspace_size(rows, d), dtype=torch.uint8, device="cuda")
+    want = [torch.empty_like(t["dy"]), *(torch.empty(d, dtype=F32, device="cuda") for _ in range(2))]
+    lsq.lsq_layernorm_bwd(t["dy"], t["x"], t["g"], mean, rstd, t["res"], *want, 0, rows, d, ws)
+    dy, dg, db = torch.empty_like(t["dy"]), torch.empty_like(want[1]), torch.empty_like(want[2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dy.copy_(t["dy"])
+        lsq.lsq_layernorm_bwd(dy, t["x"], t["g"], mean, rstd, t["res"], dy, dg, db, 0, rows, d, ws)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((dy, dg, db), want))

@@ -15,10 +15,10 @@
 // tiles: bound by what L2 feeds an SM, and below that by start and exchange; dx and dW share a launch there)
 // and a persistent CTA-pair form (many tiles: bound by the tensor cores, in a
 // long run by the power cap); plan_product picks by a measured cost model.
-// Measured on B200 (graph replays): 2048 x 14336 x 4096 forward 153-156 us with
+// Measured on B200 (graph replays): 2048 x 14336 x 4096 forward 155-157 us with
 // any activation (1.55 PFLOP/s; 138 us and 86% of the tensor pipe in isolation
-// at full clock), 188 with bias, residual and z kept, dx 165, dW 166;
-// 333 x 1536 x 576 6.0; 1 x 4096 x 4096 8.0 with the weight from HBM.
+// at full clock), 171 with bias, residual and z kept, dx 163, dW 168;
+// 333 x 1536 x 576 4.7; 1 x 4096 x 4096 7.4 with the weight from HBM.
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
@@ -703,7 +703,7 @@ static lsq_status launch_pair(const GMaps& maps, const Params& p, int64_t tiles,
 // multiplies 16-byte words of the eight weight rows with the row's words of x in f32x2, and the warps' sums
 // join in shared memory in warp order.  Eight 16-byte loads a lane and step are in flight, and four blocks run on
 // an SM (4096 x 4096 7.4 us with three, 6.4 with four, over three weights that L2 holds in part).  Weights from HBM,
-// graph replays, against the tiles above: 4096 x 4096 8.0 us (8.9), 14336 x 4096 21.7 (22.6), 576 x 1536 2.4
+// graph replays, against the tiles above: 4096 x 4096 7.4 us (8.9), 14336 x 4096 21.5 (22.6), 576 x 1536 2.4
 // (3.8); the same kernel with two rows loses from 1 M weights on (13.5 us for 9.0: its products take over).
 struct OneRow {
   const uint4 *x, *w;
@@ -1012,6 +1012,7 @@ __global__ void __launch_bounds__(256, 4) dz_kernel(const uint4* __restrict__ dy
 struct Strips {
   int64_t rows;
   int n, joined;
+  int64_t most;  // the rows of partial sums that the workspace has: no fewer for more rows, as n may be
 };
 static Strips strips_of(int64_t M, int64_t N, int act) {
   const int64_t cb = (N + 255) / 256, slots = 4 * num_sms();
@@ -1021,6 +1022,7 @@ static Strips strips_of(int64_t M, int64_t N, int act) {
   s.rows = std::max<int64_t>(8, (M + want - 1) / want);
   s.n = (int)((M + s.rows - 1) / s.rows);
   s.joined = s.n <= 8;
+  s.most = std::min<int64_t>((M + 7) / 8, want);
   return s;
 }
 static size_t round256(size_t b) { return (b + 255) / 256 * 256; }
@@ -1073,7 +1075,7 @@ extern "C" lsq_status lsq_linear_fwd(const void* x, const void* w, const void* b
 extern "C" size_t lsq_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act) {
   if (M < 1 || N < 8 || K < 8) return 256;
   return (act == LSQ_ACT_NONE ? 0 : lin::round256((size_t)M * (size_t)N * 2)) +
-         lin::round256((size_t)lin::strips_of(M, N, act).n * (size_t)N * sizeof(float));
+         lin::round256((size_t)lin::strips_of(M, N, act).most * (size_t)N * sizeof(float));
 }
 
 extern "C" lsq_status lsq_linear_bwd(const void* dy, const void* x, const void* w, const void* z, int32_t act, void* dx,

@@ -179,3 +179,14 @@ def test_linear_backward_refuses_every_overlap():
             v = list(a)
             v[out] = v[other]
             assert fn(*v[:4], 2, v[4], v[5], 1, v[6], 0, 4, 64, 64, v[7], need, S) == EINVAL, (out, other)
+
+
+@pytest.mark.parametrize("act", [0, 2])
+def test_a_workspace_for_more_rows_serves_fewer(act):
+    """Sized once for the largest batch, as a ragged run does it."""
+    for N in (8, 576, 1000, 4096, 40000):
+        sizes = [L.lsq_linear_bwd_workspace_size(M, N, 64, act) for M in (*range(1, 1200), *range(4700, 4800), 9000)]
+        assert sizes == sorted(sizes), N
+    for d in (8, 64, 576, 2048, 5120, 16384):
+        sizes = [L.lsq_layernorm_bwd_workspace_size(r, d) for r in (*range(1, 3100), 5000, 9000)]
+        assert sizes == sorted(sizes), d

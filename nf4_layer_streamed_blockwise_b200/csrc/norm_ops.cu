@@ -13,8 +13,8 @@
 // (5.3 TB/s: its two dependent reductions a row), backward with frozen gain
 // 53.0 (6.3 TB/s), with dg and db 61.3 (the 12 MB of partial sums and their
 // second kernel), norm and checkpoint 35.2 (6.0), restore and norm 34.1 (6.2),
-// backward from the checkpoint 50.8 (5.8).  2048 x 4096: 8.2, 15.6, 21.2, 9.2,
-// 8.5, 11.6 us.  One row of 4096: 2.2 us, launch and latency.
+// backward from the checkpoint 50.8 (5.8).  2048 x 4096: 8.6, 15.6, 19.5, 9.0,
+// 8.5, 11.6 us.  One row of 4096: 1.6 us, launch and latency.
 #include <algorithm>
 
 #include "common.cuh"

@@ -283,7 +283,8 @@ struct Bwd {
 
 // RMSNorm from a checkpoint: out = res + rs (dy g) - x rs^3 mean(dy g x), one row per warp or block
 template <int V, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) rms_bwd_unpack8_kernel(const __grid_constant__ Bwd p) {
+__global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024)
+    rms_bwd_unpack8_kernel(const __grid_constant__ Bwd p) {
   __shared__ float red[32];
   const int T = WARP ? 32 : (int)blockDim.x;
   const int t = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
@@ -337,8 +338,9 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) rms_bwd_unpa
 
 // LayerNorm: out = res + rs (a - mean(a) - xh mean(a xh)), a = dy g, xh = (x - mean) rs.  Warps (d <= 768)
 // or blocks walk the rows in strides and a thread's columns stay the same, so the sums over rows of dy xh
-// and dy (dg, db) collect in registers and leave once per block; col_sum_kernel adds the blocks in order.  Few rows
-// have a kernel of their own.  The arithmetic runs on pairs (f32x2): scalar, its 30 operations an element took as long as the loads.
+// and dy (dg, db) collect in registers and leave once per block; col_sum_kernel adds the blocks in order.  Few
+// rows have a kernel of their own.  The arithmetic runs on pairs (f32x2): scalar, its 30 operations an element took
+// as long as the loads.
 
 // one word of the first pass: xh and a, their row sums, and the column sums of dy xh and dy
 template <bool GRADS>

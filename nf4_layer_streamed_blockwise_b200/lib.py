@@ -595,12 +595,16 @@ def _t(fn: str, name: str, t, dtype, n: int, dev: int) -> Optional[int]:
 
 
 _cur_dev = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_cuda_up = False
 
 
 def _here(stream):
     """The current device's index (-2, no tensor's, before CUDA is up) and the stream's handle."""
-    if not torch.cuda.is_initialized():
-        return -2, _stream(stream)
+    global _cuda_up
+    if not _cuda_up:
+        if not torch.cuda.is_initialized():
+            return -2, _stream(stream)
+        _cuda_up = True
     dev = _cur_dev()
     return dev, _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 

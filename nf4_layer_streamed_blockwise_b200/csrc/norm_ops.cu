@@ -834,9 +834,16 @@ static lsq_status run_ln_bwd_few(const Bwd& p, bool grads, cudaStream_t s) {
                 : (d8 <= 256   ? ln_bwd_few_kernel<1, false>
                    : d8 <= 512 ? ln_bwd_few_kernel<2, false>
                                : ln_bwd_few_kernel<4, false>);
-  // the widest column blocks that leave a thread no more than two rows, at least 32 columns (64 bytes of a row)
-  int seg = 5;
-  while (seg > 2 && p.rows > 2 * (int64_t)(threads >> seg)) --seg;
+  // Column blocks of 32 to 256 columns (64 bytes of a row at least): a block costs its place about 2.5 us, a row of
+  // a thread 0.12.  With 32 / 64 / 128 / 256 columns: 333 x 576 3.1 / 3.5 / 4.4 / 6.8 us, 333 x 5120 5.5 / 4.2 / 5.1 /
+  // 7.3, 130 x 16384 11.7 / 7.8 / 5.6 / 5.7.
+  const int slots = num_sms() * (threads == 512 ? 1 : d8 > 512 || (warp && d8 > 64) ? 2 : 4);
+  int seg = 2;
+  double least = 1e30;
+  for (int i = 2; i <= 5; ++i) {
+    const double us = 2.5 * ((d8 + (1 << i) - 1) >> i) / slots + 0.12 * (double)(p.rows << i) / threads;
+    if (us < least) least = us, seg = i;
+  }
   const int cols = grads ? (d8 + (1 << seg) - 1) >> seg : 0;
   const size_t smem = (size_t)(threads / 32) * FEW_PITCH * sizeof(float) << seg;
   const unsigned rows = (unsigned)(warp ? (p.rows + 7) / 8 : p.rows);

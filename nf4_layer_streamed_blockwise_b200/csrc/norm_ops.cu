@@ -145,7 +145,8 @@ struct Fwd {
   float inv_d, eps;
 };
 
-template <int V, bool WARP, int SRC, int NORM, bool PACK>
+// AHEAD: gain and bias are under way with x, not behind the row's sums
+template <int V, bool WARP, int SRC, int NORM, bool PACK, bool AHEAD>
 __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) row_fwd_kernel(const __grid_constant__ Fwd p) {
   __shared__ float red[2][32];
   const int T = WARP ? 32 : (int)blockDim.x;
@@ -180,9 +181,6 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 4 ? 512 : 1024) row_fwd_kern
       if (c < d8) p.xo[base + c] = xv[i];
     }
   }
-  // short rows' gain and bias are under way with x, not behind the row's sums (one row of 4096: 1.6 us, not
-  // 1.8; with two words a thread the registers cost more: 8192 x 5120 39.5 us for 34.8)
-  constexpr bool AHEAD = NORM != NONE && V == 1;
   uint4 gv[AHEAD ? V : 1], bv[AHEAD && NORM == LAYER ? V : 1];
   auto gain = [&](int c) { return c < d8 ? p.g[c] : make_uint4(0u, 0u, 0u, 0u); };
   auto bias = [&](int c) { return c < d8 && p.b ? p.b[c] : make_uint4(0u, 0u, 0u, 0u); };
@@ -722,9 +720,12 @@ lsq_status col_sum(const float* part, int G, int64_t ld, int64_t n0, int64_t nco
 // 600 x 4096 (1.0) 3.8 and 3.7 with four.  More rows, for 8192 x 5120 with 1 / 2 / 4 words: norm and checkpoint
 // 46.7 / 35.0 / 36.4 us, restore and norm 42.7 / 34.2 / 34.9; LayerNorm's two reductions a row ask for fewer
 // threads in each (46.7 / 37.8 / 31.7), the backward's three arrays for fewer registers (50.8 / 57.9 / 60.3).
+// Gain and bias are fetched ahead where the row's latency decides, one row of 4096 1.6 us for 1.8, 64 x 576 1.5 for
+// 2.0; among many rows the registers cost more (16384 x 576 11.1 for 10.6, norm and checkpoint of 200 x 16384 5.7 for
+// 4.8 and of 8192 x 5120 39.5 for 34.8).
 enum Pass { FORWARD, LAYERNORM, BACKWARD };
 struct Geo {
-  int v, threads, warp;
+  int v, threads, warp, ahead;
   unsigned blocks;
 };
 static Geo row_geo(int64_t rows, int d8, Pass pass) {
@@ -733,6 +734,7 @@ static Geo row_geo(int64_t rows, int d8, Pass pass) {
   if (g.warp) {
     g.v = d8 <= 32 ? 1 : d8 <= 64 ? 2 : 4;
     g.threads = rows >= 4 * num_sms() ? 256 : 64;
+    g.ahead = g.v == 1 || g.threads == 64;
     const int per = g.threads / 32;
     g.blocks = (unsigned)((rows + per - 1) / per);
     return g;
@@ -742,6 +744,7 @@ static Geo row_geo(int64_t rows, int d8, Pass pass) {
       rows >= 2 * num_sms() && (pass == LAYERNORM ? rows * d8 > round : pass == FORWARD && 3 * rows * d8 > 4 * round);
   g.v = d8 > 1024 ? (many ? 4 : 2) : many && d8 >= 512 && pass == LAYERNORM ? 4 : many && d8 >= 256 ? 2 : 1;
   g.threads = (((d8 + g.v - 1) / g.v) + 31) / 32 * 32;
+  g.ahead = g.v == 1 || (!many && rows <= num_sms() * (1120 / g.threads));  // the registers' one round
   g.blocks = (unsigned)rows;
   return g;
 }
@@ -795,12 +798,16 @@ static lsq_status run_fwd(Fwd p, int64_t rows, int64_t d, const char* what, cuda
   p.nb = (int)((d + 63) / 64);
   p.inv_d = 1.0f / (float)d;
   const Geo g = row_geo(rows, p.d8, NORM == LAYER ? LAYERNORM : FORWARD);
-  auto k = g.warp ? (g.v == 1   ? row_fwd_kernel<1, true, SRC, NORM, PACK>
-                     : g.v == 2 ? row_fwd_kernel<2, true, SRC, NORM, PACK>
-                                : row_fwd_kernel<4, true, SRC, NORM, PACK>)
-                  : (g.v == 1   ? row_fwd_kernel<1, false, SRC, NORM, PACK>
-                     : g.v == 2 ? row_fwd_kernel<2, false, SRC, NORM, PACK>
-                                : row_fwd_kernel<4, false, SRC, NORM, PACK>);
+  constexpr bool N = NORM != NONE;  // without a norm there is nothing to fetch ahead
+  auto k = g.warp ? (g.v == 1   ? row_fwd_kernel<1, true, SRC, NORM, PACK, N>
+                     : g.v == 2 ? (g.ahead ? row_fwd_kernel<2, true, SRC, NORM, PACK, N>
+                                           : row_fwd_kernel<2, true, SRC, NORM, PACK, false>)
+                                : (g.ahead ? row_fwd_kernel<4, true, SRC, NORM, PACK, N>
+                                           : row_fwd_kernel<4, true, SRC, NORM, PACK, false>))
+                  : (g.v == 1   ? row_fwd_kernel<1, false, SRC, NORM, PACK, N>
+                     : g.v == 2 ? (g.ahead ? row_fwd_kernel<2, false, SRC, NORM, PACK, N>
+                                           : row_fwd_kernel<2, false, SRC, NORM, PACK, false>)
+                                : row_fwd_kernel<4, false, SRC, NORM, PACK, false>);
   return launch_chained(what, k, dim3(g.blocks), (unsigned)g.threads, 0, 1, s, p);
 }
 template <int V, bool WARP, bool GRADS>

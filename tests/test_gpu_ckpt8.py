@@ -149,3 +149,8 @@ def test_more_rows_than_run_at_once(lsq, rows, d):
     """Two and four words a thread, and both sides of where they begin."""
     test_bit_exact(lsq, rows, d)
     test_fused_passes_equal_their_parts(lsq, rows, d)
+
+
+@pytest.mark.parametrize("rows,d", [(592, 776), (591, 1024), (592, 264), (148, 16384), (149, 8328)])
+def test_where_the_fetch_ahead_ends(lsq, rows, d):
+    test_fused_passes_equal_their_parts(lsq, rows, d)

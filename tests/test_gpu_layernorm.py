@@ -211,3 +211,9 @@ def test_few_rows_captured_in_place(lsq):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((dy, dg, db), want))
+
+
+@pytest.mark.parametrize("rows,d", [(592, 576), (591, 576), (700, 1024), (592, 264), (148, 16384), (149, 16384)])
+def test_forward_where_the_fetch_ahead_ends(lsq, rows, d):
+    test_forward(lsq, rows, d, True)
+    test_forward(lsq, rows, d, False)

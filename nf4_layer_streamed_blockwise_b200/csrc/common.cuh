@@ -103,7 +103,9 @@ __device__ __forceinline__ void mbar_drain(uint64_t* full, int stages, int s, ui
 // A kernel launched by launch_chained (host_common.h) may start while its predecessor on the stream still
 // runs: it sets up (shared memory, barriers, tensor memory), calls grid_wait before its first access to global
 // memory, which returns once the predecessor has finished and its writes are visible, and calls grid_release
-// so that its own successor may do the same.  Every thread that touches global memory calls grid_wait.
+// so that its own successor may do the same.  Every thread that touches global memory calls grid_wait, and none of
+// its pointers is __restrict__ to const, nor read by __ldg or ld.global.nc: those declare memory that nobody writes
+// while the kernel runs, which its predecessor still does, and such a load is not held behind grid_wait.
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(512) ln_bwd_few_kernel(const __grid_constant__
 // out0[c] (+)= sum over the G rows of part[.][c] for c < n0, out1[c - n0] for the columns from n0 on
 // (either may be null; n0 and ncols even); part has row stride ld.  Warp w of 32 takes rows w, w + 32, ...,
 // ten loads in flight (two blocks' rows on 148 SMs are one batch); then warp w adds column pair w's 32 sums.
-__global__ void __launch_bounds__(1024) col_sum_kernel(const float* __restrict__ part, int G, int64_t ld, int64_t n0,
+__global__ void __launch_bounds__(1024) col_sum_kernel(const float* part, int G, int64_t ld, int64_t n0,
                                                        int64_t ncols, float* out0, float* out1, int accumulate) {
   __shared__ float2 s[32][33];
   grid_release();

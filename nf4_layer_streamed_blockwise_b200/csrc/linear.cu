@@ -48,11 +48,12 @@ __device__ __forceinline__ bool elect_one() {
 
 // ---------------------------------------------------------------- activations
 // act(z) and act'(z) in fp32 on the fp32 pre-activation, two values at a time (f32x2; scalar, the derivative
-// of GELU took longer than its bytes: 67 us, not 53, for 8192 x 5120), through the special-function unit's
-// exp2 and reciprocal (relative error about 2^-22, far below the bf16 rounding that follows; the sums of
-// dbias see it as 2^-22 of their terms).  The logistic under- and overflows to the right limits; what would
-// meet 0 * inf is taken out at the end.  GELU's normal distribution function is Abramowitz & Stegun 7.1.26
-// (|error| <= 1.5e-7 in erf), whose exponential is the density that the derivative needs.
+// of GELU took longer than its bytes), through the special-function unit's exp2 and reciprocal (relative error
+// about 2^-22).  Relative to the result they are off by at most 2^-12, a sixteenth of half a bf16 step, for negative
+// z too: the rounding of exp2's argument, up to 126 in size, is 2e-5 of it and the fit of the normal tail 1e-4;
+// derivatives by 2^-11 from z = -2 down, and near their zero by 1e-6 in absolute terms.  Factors below 2^-126 are
+// flushed to 0 (SiLU from z = -87.3 down, the two GELUs from -13.2 and -10).  The logistic under- and overflows to
+// the right limits; what would meet 0 * inf is taken out at the end.
 __device__ __forceinline__ float ex2_f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -80,18 +81,22 @@ __device__ __forceinline__ uint64_t logistic2(uint64_t v) { return rcp_2(add2(ex
 __device__ __forceinline__ uint64_t gelu_tanh_arg(uint64_t z) {
   return mul2(z, fma2(mul2(z, z), both(-LOG2E * GT_C * GT_A), both(-LOG2E * GT_C)));
 }
-// Phi(z); e = exp(-z^2 / 2)
+// Phi(z); e = exp(-z^2 / 2).  The tail Phi(-|z|) = e R(|z|) is computed itself and only subtracted from 1 for z > 0, so
+// small results keep their relative accuracy: formed as 1/2 - (1/2 - tail) it is off by 4% at z = -5.  R(a) =
+// erfcx(a / sqrt 2) / 2 as t q(t), t = 1 / (1 + 0.29 a), q of degree 5: an own fit, weighted minimax over 0 <= a <= 13.3
+// (where e reaches 2^-126), off by at most 4.8e-8 / e in absolute and 1e-4 in relative terms.
 __device__ __forceinline__ uint64_t normal_cdf2(uint64_t z, uint64_t& e) {
   const uint64_t az = z & 0x7fffffff7fffffffull;
-  const uint64_t t = rcp_2(fma2(az, both(0.3275911f * 0.70710678118654752f), both(1.0f)));
-  uint64_t q = fma2(both(1.061405429f * 0.5f), t, both(-1.453152027f * 0.5f));
-  q = fma2(q, t, both(1.421413741f * 0.5f));
-  q = fma2(q, t, both(-0.284496736f * 0.5f));
-  q = fma2(q, t, both(0.254829592f * 0.5f));
+  const uint64_t t = rcp_2(fma2(az, both(0.29f), both(1.0f)));
+  uint64_t q = fma2(both(-0.08963339f), t, both(0.28783932f));
+  q = fma2(q, t, both(-0.09734405f));
+  q = fma2(q, t, both(0.18232992f));
+  q = fma2(q, t, both(0.09983516f));
+  q = fma2(q, t, both(0.11697299f));
   e = ex2_2(mul2(mul2(z, z), both(-0.5f * LOG2E)));
-  // Phi = 1/2 +- (1/2 - Phi(-|z|)), the sign z's
-  const uint64_t h = fma2(mul2(q, t), e ^ 0x8000000080000000ull, both(0.5f));
-  return add2(both(0.5f), h ^ (z & 0x8000000080000000ull));
+  const uint64_t tail = mul2(mul2(q, t), e);
+  const int lo = (int)(uint32_t)z, hi = (int)(uint32_t)(z >> 32);  // by the sign bit, -0 too: 0 + tail or 1 - tail
+  return add2(f2(lo < 0 ? 0.0f : 1.0f, hi < 0 ? 0.0f : 1.0f), tail ^ (~z & 0x8000000080000000ull));
 }
 template <int ACT>
 __device__ __forceinline__ uint64_t act2(uint64_t z) {

@@ -470,6 +470,10 @@ lsq_status lsq_lora_refresh_bf16(const float* p, void* p_bf16, int64_t n, lsq_cu
  * feature counts d, N, K multiples of 8; anything else is EINVAL before
  * anything is enqueued.
  * ---------------------------------------------------------------------- */
+/* Kernels that this section's calls have enqueued in this process, captured
+ * ones included (once, when captured).  Its calls choose between one kernel
+ * and several by sizes and arguments; this is what they did. */
+uint64_t lsq_launch_count(void);
 /* LayerNorm: y = (x - mean) rstd g + b per row, mean and variance over d,
  * rstd = 1 / sqrt(var + eps) (variance of the centred values, no cancellation).
  *  x, y     bf16 [rows, d], y may be x;  g, b bf16 [d] (b may be NULL: no bias)

@@ -10,6 +10,8 @@
 
 namespace lsq {
 
+std::atomic<uint64_t> g_launches{0};
+
 static thread_local char t_msg[512] = "";
 
 lsq_status fail(lsq_status s, const char* fmt, ...) {
@@ -212,6 +214,8 @@ const char* lsq_status_str(lsq_status s) {
 const char* lsq_last_error(void) { return lsq::t_msg; }
 
 int lsq_version(void) { return 100; }
+
+uint64_t lsq_launch_count(void) { return lsq::g_launches.load(std::memory_order_relaxed); }
 
 lsq_status lsq_wait_flag(const uint64_t* flag, uint64_t value, int64_t limit_ns, lsq_cuda_stream stream) {
   if (!flag || !lsq::aligned(flag, 8)) return lsq::fail(LSQ_EINVAL, "lsq_wait_flag: flag NULL or not 8-byte aligned");

@@ -7,6 +7,8 @@
 #include <stdarg.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/lsq.h"
 
 namespace lsq {
@@ -39,6 +41,8 @@ inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 int num_sms();
 
+extern std::atomic<uint64_t> g_launches;  // kernels that launch_chained has enqueued
+
 // Launch with programmatic stream serialization (and a cluster size, where above 1): the kernel may be set up
 // while its predecessor on the stream still runs, so it must call grid_wait (common.cuh).
 template <typename... P, typename... A>
@@ -58,7 +62,9 @@ lsq_status launch_chained(const char* what, void (*kernel)(P...), dim3 grid, uns
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-  return e == cudaSuccess ? LSQ_OK : cuda_fail(e, what);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return LSQ_OK;
 }
 
 }  // namespace lsq

@@ -66,6 +66,7 @@ _SIGS = {
     "lsq_status_str": (ctypes.c_char_p, [c_int32]),
     "lsq_last_error": (ctypes.c_char_p, []),
     "lsq_version": (c_int32, []),
+    "lsq_launch_count": (ctypes.c_uint64, []),
     "lsq_device_status": (c_int32, [ctypes.POINTER(c_int32), ctypes.POINTER(c_int32)]),
     "lsq_wait_flag": (c_int32, [c_void_p, ctypes.c_uint64, c_int64, c_void_p]),
     "lsq_nf4_codebook": (c_int32, [ctypes.POINTER(c_float)]),
@@ -206,27 +207,41 @@ def _check(name: str, status: int):
         raise LsqError(status, name, msg)
 
 
-# kernel launches issued by the library, counted per call on this side
+class _Launches:
+    """Kernels that the library has launched, in [0], which can be set: those counted per call on this side, and those
+    that the library counts itself."""
+
+    def __init__(self):
+        self.counted = 0
+
+    def __getitem__(self, i):
+        return [self.counted + lsq_launch_count()][i]
+
+    def __setitem__(self, i, n):
+        if i != 0:
+            raise IndexError(i)
+        self.counted = n - lsq_launch_count()
+
+
+# counted on this side: the calls whose number of kernels follows from the call
 # (with a LoRA adapter the fused linear's forward is 2 kernels: the rank-r
 # product U = X A^T and the main GEMM, plus the operand transposition when a
 # rank state is filled, and only the main GEMM when the state is reused; the
 # backward is the operand padding (not with a state), G = dY B, the dX GEMM
 # when dx is wanted, and the dA/dB GEMM with its reduction)
-LAUNCHES = [0]
+LAUNCHES = _Launches()
 _KERNELS = {"lsq_nf4_quantize": 1, "lsq_nf4_dequantize": 1, "lsq_absmax_double_quantize": 1, "lsq_absmax_expand": 1,
             "lsq_dense_gemm": 1, "lsq_dense_gemm_ex": 1, "lsq_rmsnorm_fwd": 1, "lsq_rmsnorm_bwd": 1, "lsq_rope": 1, "lsq_rope_table": 1,
             "lsq_attention_fwd": 1, "lsq_attention_bwd": 3, "lsq_swiglu_fwd": 1, "lsq_swiglu_bwd": 1,
             "lsq_embed_gather": 1, "lsq_xent_fwd_bwd": 2, "lsq_adamw_step": 1, "lsq_lora_refresh_bf16": 1, "lsq_seq_logprob": 2,
-            "lsq_dpo_loss": 1, "lsq_seq_logprob_bwd": 1, "lsq_wait_flag": 1,
-            "lsq_layernorm_fwd": 1, "lsq_ckpt8_pack": 1, "lsq_ckpt8_unpack": 1, "lsq_rmsnorm_fwd_pack8": 1,
-            "lsq_rmsnorm_fwd_unpack8": 1, "lsq_rmsnorm_bwd_unpack8": 1, "lsq_linear_fwd": 1}
+            "lsq_dpo_loss": 1, "lsq_seq_logprob_bwd": 1, "lsq_wait_flag": 1}
 
 
 def _call(name, *args, launches=None):
     status = (_FNS.get(name) or _fn(name))(*args)
     if status:
         _check(name, status)
-    LAUNCHES[0] += _KERNELS.get(name, 0) if launches is None else launches
+    LAUNCHES.counted += _KERNELS.get(name, 0) if launches is None else launches
 
 
 def _p(t) -> Optional[int]:
@@ -283,6 +298,11 @@ def lsq_status_str(s: int) -> str:
 
 def lsq_last_error() -> str:
     return _fn("lsq_last_error")().decode(errors="replace")
+
+
+def lsq_launch_count() -> int:
+    """Kernels of the layers outside the quantised base enqueued in this process."""
+    return int(_fn("lsq_launch_count")())
 
 
 def lsq_version() -> int:
@@ -627,13 +647,11 @@ def lsq_layernorm_bwd(dy, x, g, mean, rstd, dres_in, dres_out, dg, db, accumulat
     """dres_out = dres_in + dx; dg, db fp32 (None: frozen), overwritten or (accumulate=1) added to."""
     f, n, bf, f32 = "lsq_layernorm_bwd", rows * d, torch.bfloat16, torch.float32
     dev, st = _here(stream)
-    # few rows need no second kernel
-    two = (dg is not None or db is not None) and (rows > (1024 if d < 512 else 1536) or rows * d > 1 << 23)
     _call(f, _t(f, "dy", dy, bf, n, dev), _t(f, "x", x, bf, n, dev), _t(f, "g", g, bf, d, dev),
           _t(f, "mean", mean, f32, rows, dev), _t(f, "rstd", rstd, f32, rows, dev),
           _t(f, "dres_in", dres_in, bf, n, dev), _t(f, "dres_out", dres_out, bf, n, dev), _t(f, "dg", dg, f32, d, dev),
           _t(f, "db", db, f32, d, dev), accumulate, rows, d, _t(f, "workspace", workspace, None, 0, dev),
-          _nbytes(workspace), st, launches=2 if two else 1)
+          _nbytes(workspace), st)
 
 
 def lsq_ckpt8_size(rows: int, d: int) -> int:
@@ -704,12 +722,10 @@ def lsq_linear_bwd(dy, x, w, z, act: int, dx, dw, dw_f32: int, dbias, accumulate
     """dx, dw and dbias (each may be None) of lsq_linear_fwd from dy and the kept pre-activation z."""
     f, mn, bf, f32 = "lsq_linear_bwd", M * N, torch.bfloat16, torch.float32
     dev, st = _here(stream)
-    # at least: a tall dz pass adds a kernel for dbias, and a large dx and dw take one each
-    launches = (1 if act != ACT_NONE or dbias is not None else 0) + (dx is not None or dw is not None)
     _call(f, _t(f, "dy", dy, bf, mn, dev), _t(f, "x", x, bf, M * K, dev), _t(f, "w", w, bf, N * K, dev),
           _t(f, "z", z, bf, mn, dev), act, _t(f, "dx", dx, bf, M * K, dev),
           _t(f, "dw", dw, f32 if dw_f32 else bf, N * K, dev), dw_f32, _t(f, "dbias", dbias, f32, N, dev), accumulate,
-          M, N, K, _t(f, "workspace", workspace, None, 0, dev), _nbytes(workspace), st, launches=launches)
+          M, N, K, _t(f, "workspace", workspace, None, 0, dev), _nbytes(workspace), st)
 
 
 # ---------------------------------------------------------------------------- streaming
@@ -773,7 +789,7 @@ def _with_uploads(st: int, fn):
         return fn()
     before = lsq_stream_stats(st)[0]
     out = fn()
-    LAUNCHES[0] += lsq_stream_stats(st)[0] - before
+    LAUNCHES.counted += lsq_stream_stats(st)[0] - before
     return out
 
 

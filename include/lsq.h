@@ -513,6 +513,8 @@ lsq_status lsq_ckpt8_unpack(const void* ckpt, void* x, int64_t rows, int64_t d, 
  *  fwd_unpack8: restores x (bf16, for the residual) and normalises the restored
  *               rows: y and rstd are lsq_rmsnorm_fwd's for them (rstd may be NULL)
  *  bwd_unpack8: lsq_rmsnorm_bwd with the restored rows read from the checkpoint
+ * They add a row's squares in an order of their own: rstd may differ from
+ * lsq_rmsnorm_fwd's in its last bits, and y then in a rounding.
  * dres_in may be NULL (treated as 0); dres_out may be dres_in or dy, and
  * fwd_pack8's y may be x. */
 lsq_status lsq_rmsnorm_fwd_pack8(const void* x, const void* g, void* y, float* rstd, void* ckpt, int64_t rows,

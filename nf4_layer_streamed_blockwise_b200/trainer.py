@@ -459,7 +459,10 @@ class StreamedLoraTrainer:
             A, B = self._ops(l)
         else:
             A = B = {n: None for n in S.LINEARS}
-        int8 = self.checkpoint == "int8" and hin is None   # the policy's pass, not the reference's
+        int8 = self.checkpoint == "int8"
+        # the reference's pass normalises with the policy's kernel (another order of the row's sum would make it
+        # another model: 0.05 of a sequence's log-probability at 4 layers of 576); its checkpoint is not read
+        ckpt = None if not int8 else self.ckpt[l] if hin is None else self.ckpt_ref
         if hin is None:
             hin = self.h_in if int8 and save else self._h(l)
         hout = self._h(l + 1) if hout is None else hout
@@ -482,9 +485,9 @@ class StreamedLoraTrainer:
                                          [U[n] for n in names], workspace=self.ws_lora)
 
         if int8 and save:
-            L.lsq_rmsnorm_fwd_unpack8(self.ckpt[l], W.ln1, hin, self.x1, self.rstd1, M, sh.d, sh.eps)
+            L.lsq_rmsnorm_fwd_unpack8(ckpt, W.ln1, hin, self.x1, self.rstd1, M, sh.d, sh.eps)
         elif int8:
-            L.lsq_rmsnorm_fwd_pack8(hin, W.ln1, self.x1, self.rstd1, self.ckpt[l], M, sh.d, sh.eps)
+            L.lsq_rmsnorm_fwd_pack8(hin, W.ln1, self.x1, self.rstd1, ckpt, M, sh.d, sh.eps)
         else:
             L.lsq_rmsnorm_fwd(hin, W.ln1, self.x1, self.rstd1, M, sh.d, sh.eps)
         t = self._t0()
@@ -685,6 +688,8 @@ class StreamedLoraTrainer:
         if getattr(self, "h_ref", None) is None:
             dev, M = self.x1.device, self.M
             self.h_ref = torch.empty(M, self.shape.d, dtype=torch.bfloat16, device=dev)
+            if self.checkpoint == "int8":
+                self.ckpt_ref = torch.empty(L.lsq_ckpt8_size(M, self.shape.d), dtype=torch.uint8, device=dev)
             self.row_lse = torch.empty(M, dtype=torch.float32, device=dev)
             self.pi_logp, self.ref_logp, self.dseq = (torch.empty(self.B, dtype=torch.float32, device=dev)
                                                       for _ in range(3))

@@ -959,8 +959,8 @@ __global__ void __launch_bounds__(256, 4) dz_kernel(const uint4* dy, const uint4
   uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
   if (c < n8) {
     // rows in flight, loaded before any of them is stored (the compiler may not move a load over a store that could
-    // be to the same place): with 2 / 4 rows 8192 x 5120 takes 46.7 / 44.9 us with GELU, 43.3 / 46.3 with ReLU, and
-    // 2048 x 14336 34.5 / 33.3 and 29.9 / 30.5; without an activation, where nothing is stored, 25.6 / 17.4
+    // be to the same place): with 2 / 4 rows 8192 x 5120 takes 47.6 / 45.9 us with GELU, 43.5 / 45.6 with ReLU, and
+    // 2048 x 14336 35.0 / 34.3 and 29.9 / 30.2; without an activation, where nothing is stored, 25.3 / 17.6
     constexpr int U = ACT == LSQ_ACT_RELU ? 2 : 4;
     for (int64_t r = r0 + w; r < r1; r += 8 * U) {
       uint4 dv[U], zw[U];
@@ -1026,8 +1026,9 @@ __global__ void __launch_bounds__(256, 4) dz_kernel(const uint4* dy, const uint4
 
 // row strips of dz_kernel: one round of its blocks (four per SM), at least 8 rows each; at most eight, joined in a
 // cluster, where they fill that round or a warp's rows take no longer than the second kernel: 4 with an activation
-// (M = 333, N = 1536, GELU: 5.0 us joined, 5.1 in two kernels; 512 x 1024 6.0 and 4.4; 2048 x 14336, 448 of 592
-// blocks, 43 and 38), 16 without (512 x 1024 2.8 and 3.6, 1024 x 4096 4.2 and 4.5); the host saves 2.3 us
+// (256 x 576, GELU: 4.1 us joined, 4.1 in two kernels; 333 x 1536 5.0 and 4.8; 512 x 1024 5.7 and 4.4; 2048 x 14336,
+// 448 of 592 blocks, 38.7 and 34.3), 16 without (512 x 1024 3.2 and 3.8, 1024 x 4096 4.5 and 4.5, 2048 x 4096 6.3 and
+// 5.4); the host saves 2.3 us
 struct Strips {
   int64_t rows;
   int n, joined;

@@ -2,19 +2,22 @@
 // activation checkpoint with the RMSNorm passes that write and read it.
 //
 // All are HBM-bound row passes over bf16 [rows, d].  A row belongs to one warp
-// (WARP, d <= 1024; LayerNorm backward d <= 768) or to one block; each thread
-// holds V 16-byte words of it from the one load to the last use, so every
-// input is read once.  Word c of a row belongs to thread c % T (T threads per
-// row, a multiple of 32), so eight neighbouring lanes hold one 64-column block
-// of the checkpoint.
+// (WARP, d <= 1024; d <= 768 in the LayerNorm backward's rings) or to one
+// block; each thread holds V 16-byte words of it from the one load to the last
+// use, so every input is read once from HBM (the LayerNorm backward of few
+// rows reads x and dy a second time, from L2, for its column sums; the rings
+// a second time from shared memory).  Word c of a row belongs to thread c % T
+// (T threads per row, a multiple of 32), so eight neighbouring lanes hold one
+// 64-column block of the checkpoint.
 //
 // Measured on B200 in graph replays over three sets of buffers, 8192 x 5120
-// (a copy of the same tensor runs at 6.1 TB/s): LayerNorm forward 31.4 us
+// (a copy of the same tensor runs at 6.1 TB/s): LayerNorm forward 31.9 us
 // (5.3 TB/s: its two dependent reductions a row), backward with frozen gain
-// 53.0 (6.3 TB/s), with dg and db 61.3 (the 12 MB of partial sums and their
-// second kernel), norm and checkpoint 35.2 (6.0), restore and norm 34.1 (6.2),
-// backward from the checkpoint 50.8 (5.8).  2048 x 4096: 8.6, 15.6, 19.5, 9.0,
-// 8.5, 11.6 us.  One row of 4096: 1.6 us, launch and latency.
+// 53.1 (6.3 TB/s), with dg and db 61.4 (the 12 MB of partial sums and their
+// second kernel), checkpoint alone 21.2 (6.0), restored alone 20.5 (6.2), norm
+// and checkpoint 35.4 (6.0), restore and norm 34.7 (6.1), backward from the
+// checkpoint 51.4 (5.7).  2048 x 4096: 8.2, 15.9, 21.6, 4.8, 4.0, 9.4, 8.4,
+// 11.8 us.  One row of 4096: 1.6 us, launch and latency.
 #include <algorithm>
 
 #include "common.cuh"
